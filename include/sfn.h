@@ -2,7 +2,9 @@
  * sfn.h -- C ABI of libsfn: the predictor-gated bank-wise top-k sparse
  * SwiGLU FFN on NVIDIA B200 (sm_100a) -- its forward pass (whole layer or one
  * bank shard), its backward with the surrogate top-k gradient, and the
- * pages' Dense-4x comparison.
+ * pages' Dense-4x comparison -- and the operators of its coarse counterpart,
+ * whole SwiGLU experts in place of channels: routing to experts with its
+ * gradient, the product in 8-bit integers, and the experts' products.
  *
  * The method: "Continual LLM Upcycling: A Predictor-Gated Bank-Wise Sparsity
  * Training Recipe for Dense-to-Sparse LLMs" (arXiv 2606.10722).  Passages are
@@ -308,6 +310,110 @@ sfn_status sfn_sparse_ffn_backward(const void *x, const void *A, const void *B, 
                                    void *workspace, size_t workspace_bytes,
                                    sfn_stream_t stream);
 
+/*
+ * Routing of tokens to experts: which k of E experts a token goes to, and
+ * with which weights.  For a token's logits l [E]:
+ *   s = softmax(l) (SFN_SCORE_SOFTMAX) or 1 / (1 + exp(-l)) (SFN_SCORE_SIGMOID)
+ *   c = s + bias, and -inf where l or bias is -inf.  The bias (a balance bias;
+ *       float32 [E], may be NULL: 0) takes part in the choice only.
+ *   The experts are `groups` contiguous groups of E / groups.  A group's score
+ *       is its largest c (group_top 1) or the sum of its two largest (2),
+ *       those at -inf left out; the top_groups best groups stay (ties to the
+ *       lower group).  groups = top_groups = 1: no restriction.
+ *   Of the experts that stay, the k of largest c, in descending order, equal
+ *       ones to the lower index; NaN ranks below every number.
+ *   w_i = scale s_i / (sum over the k of s) if renormalize (0 where that sum
+ *       is 0), else scale s_i.
+ * A slot left without an expert (its c is -inf: the token's mask leaves fewer
+ * than k) is empty: expert -1, weight 0.  A row of -inf has softmax scores 0.
+ * Under softmax a NaN or +inf logit makes every score and weight of its row
+ * NaN.
+ *
+ * The choice does not depend on rounding: without a bias experts are ranked
+ * by their logits, else by c as float64 gives it, so the same logits choose
+ * the same experts in every call, whatever the batch around them.
+ *
+ * logits [T][E] in `dtype`; experts int32 [T][k]; weights float32 [T][k];
+ * scores (may be NULL) receives s, float32 [T][E].  1 <= k <= 32, E <= 1024,
+ * groups <= 32 (else SFN_ERR_UNSUPPORTED); groups divides E, k <= top_groups *
+ * E / groups, group_top 1 or 2, scale finite (else SFN_ERR_INVALID_VALUE).
+ * Pointers need the alignment of their element type only.
+ */
+typedef enum sfn_score { SFN_SCORE_SOFTMAX = 0, SFN_SCORE_SIGMOID = 1 } sfn_score;
+sfn_status sfn_route_experts(const void *logits, sfn_dtype dtype, const float *bias,
+                             int32_t *experts, float *weights, float *scores, int64_t T, int E,
+                             int k, sfn_score score, int groups, int top_groups, int group_top,
+                             int renormalize, float scale, sfn_stream_t stream);
+
+/*
+ * Gradient of sfn_route_experts: dlogits [T][E] (in `dtype`, overwritten) for
+ * dweights = dL/dw [T][k] and, if not NULL, dscores = dL/ds [T][E] (a balance
+ * loss on the scores), both float32.  The choice itself, and with it the bias,
+ * has no gradient.  logits and experts are the forward's; -1 marks an empty
+ * slot, and an expert that is in two slots gets the sum of both.  An index
+ * outside [-1, E) is taken as empty.  Sums in float32, one rounding at the end.
+ */
+sfn_status sfn_route_experts_backward(const void *logits, sfn_dtype dtype,
+                                      const int32_t *experts, const float *dweights,
+                                      const float *dscores, void *dlogits, int64_t T, int E,
+                                      int k, sfn_score score, int renormalize, float scale,
+                                      sfn_stream_t stream);
+
+/*
+ * Symmetric 8-bit quantisation of the rows of x [T][K] (`dtype`): scale[t] =
+ * max |x_t| / 127 (float32), q[t] = rint(127 x_t / max |x_t|), halves to even.
+ * A row of zeros has scale 0 and q 0; a row with an infinity or a NaN has
+ * scale NaN and q 0.  For tokens (a scale each) and for weight rows (a scale
+ * for each output channel) alike.  K a multiple of 16 up to 131072.
+ */
+sfn_status sfn_quantize_rows_i8(const void *x, sfn_dtype dtype, int8_t *q, float *scale,
+                                int64_t T, int K, sfn_stream_t stream);
+
+/*
+ * Product in 8-bit integers with a scale for each token and output channel:
+ *   y[t][n] = x_scale[t] w_scale[n] sum_k xq[t][k] wq[n][k]
+ * with the sum exact in 32 bits; xq [T][K], wq [N][K] (an nn.Linear weight,
+ * quantised by sfn_quantize_rows_i8), y [T][N] in y_dtype.  Any T and N, K a
+ * multiple of 16 (else SFN_ERR_MISALIGNED) up to 131072 (else
+ * SFN_ERR_UNSUPPORTED), the length at which 127^2 K still fits 32 bits; values
+ * of -128 are allowed up to K = 131056.
+ */
+sfn_status sfn_matmul_i8(const int8_t *xq, const float *x_scale, const int8_t *wq,
+                         const float *w_scale, void *y, sfn_dtype y_dtype, int64_t T, int N,
+                         int K, sfn_stream_t stream);
+
+/*
+ * The two in one: y = quantise(x) by wq, x [T][K] in x_dtype.  Scratch: at
+ * least sfn_linear_i8_workspace_bytes() bytes, 256-byte aligned.
+ */
+size_t sfn_linear_i8_workspace_bytes(int64_t T, int K);
+sfn_status sfn_linear_i8(const void *x, sfn_dtype x_dtype, const int8_t *wq,
+                         const float *w_scale, void *y, sfn_dtype y_dtype, int64_t T, int N,
+                         int K, void *workspace, size_t workspace_bytes, sfn_stream_t stream);
+
+/*
+ * The products of the experts that tokens were routed to, in 8-bit integers:
+ * for slot i of token t with expert e = experts[t][i] and weight w,
+ *   g = Wg[e] x_t,  u = Wu[e] x_t        (products as in sfn_linear_i8)
+ *   h = silu(g) u, rounded to bf16, then quantised as a row of its own
+ *   y_t = sum_i w_i (Wd[e] h_i), summed in float32, rounded to bf16
+ * x, y bf16 [T][d]; experts int32 and weights float32 [T][k] as
+ * sfn_route_experts gives them (a slot of -1 adds nothing; an expert may be
+ * in several slots; an index >= E adds nothing and sets bit 2 of the device
+ * error word).  Wg, Wu int8 [E][f][d] with scales float32 [E][f]; Wd int8
+ * [E][d][f] with scales [E][d]: here the down projection is in nn.Linear's
+ * layout, not channel-major, so that each output channel has a scale.
+ * d and f multiples of 16 (else SFN_ERR_MISALIGNED); 1 <= k <= 32, E <= 1024,
+ * T k < 2^31 (else SFN_ERR_UNSUPPORTED).  Scratch: at least
+ * sfn_experts_i8_workspace_bytes() bytes, 256-byte aligned.
+ */
+size_t sfn_experts_i8_workspace_bytes(int64_t T, int E, int k, int d, int f);
+sfn_status sfn_experts_i8_forward(const void *x, const int32_t *experts, const float *weights,
+                                  const int8_t *Wg, const float *sg, const int8_t *Wu,
+                                  const float *su, const int8_t *Wd, const float *sd, void *y,
+                                  int64_t T, int E, int k, int d, int f, void *workspace,
+                                  size_t workspace_bytes, sfn_stream_t stream);
+
 /* float32 twins of the two forward entry points. */
 sfn_status sfn_sparse_ffn_forward_f32(const float *x, const float *A, const float *B,
                                       const float *Wg, const float *Wu, const float *Wd,
@@ -339,10 +445,13 @@ enum {
   SFN_STAGE_TC_LOGITS_TOPK = 6, /* tensor cores: logits + fused top-k   */
   SFN_STAGE_TC_GATEUP = 7,    /* tensor cores: masked sigma(p) g u      */
   SFN_STAGE_TC_DOWN = 8,      /* tensor cores: y = act W_down           */
+  SFN_STAGE_ROUTE = 9,        /* routing to experts and its gradient    */
   SFN_STAGE_DENSE4X_GATEUP = 10, /* Dense-4x: silu(g) u + amplitude top-k */
   SFN_STAGE_BWD_TAU = 11,     /* backward: mask and thresholds          */
   SFN_STAGE_BWD_ELEM = 12,    /* backward: surrogate chain rule         */
   SFN_STAGE_BWD_GEMM = 13,    /* backward: tensor-core contractions     */
+  SFN_STAGE_I8_PRODUCT = 14,  /* products in 8-bit integers             */
+  SFN_STAGE_I8_ROWS = 15,     /* quantisation, row plan, weighted sums  */
   SFN_STAGE_COUNT = 16        /* room for the stage ids of this library */
 };
 sfn_status sfn_timing_begin(void);

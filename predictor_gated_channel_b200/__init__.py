@@ -1,4 +1,6 @@
-"""Predictor-gated bank-wise top-k sparse SwiGLU FFN forward on B200 (sm_100a).
+"""Predictor-gated bank-wise top-k sparse SwiGLU FFN forward on B200 (sm_100a), and the
+operators of its coarse counterpart: routing to whole SwiGLU experts, the product in 8-bit
+integers, and the experts' products.
 
 Thin PyTorch-facing binding of the C ABI in ``include/sfn.h``: these functions
 only check tensors and pass their device pointers and the current CUDA stream
@@ -16,7 +18,9 @@ from . import _capi
 from ._capi import SfnError
 
 __all__ = ["predict", "bank_topk", "sparse_ffn_forward", "dense4x_forward", "workspace_bytes",
-           "kernel_launch_count", "SfnError"]
+           "route_experts", "route_experts_backward", "quantize_rows_i8", "matmul_i8",
+           "linear_i8", "linear_i8_workspace_bytes", "experts_i8_forward",
+           "experts_i8_workspace_bytes", "kernel_launch_count", "SfnError"]
 
 
 def _torch():
@@ -258,3 +262,216 @@ def sparse_ffn_backward(x, A, B, Wg, Wu, Wd, dy, bank: int = 64, k: int = 16,
         workspace.data_ptr(), workspace.numel() * workspace.element_size(),
         _stream_ptr(stream, x.device)), "sfn_sparse_ffn_backward")
     return out
+
+
+# ---------------------------------------------------------------- expert operators
+SCORES = {"softmax": _capi.SFN_SCORE_SOFTMAX, "sigmoid": _capi.SFN_SCORE_SIGMOID}
+
+
+def _arg(t, name, where, device, shape, dtypes):
+    """A contiguous CUDA tensor on `device` of this shape and one of these dtypes."""
+    _dev(t, name)
+    if t.device != device:
+        raise ValueError(f"{where}: {name} is on {t.device}, not on {device}")
+    if tuple(t.shape) != tuple(shape) or t.dtype not in dtypes:
+        raise ValueError(f"{where}: {name} must be {list(shape)} of "
+                         f"{' or '.join(str(d) for d in dtypes)}, not {list(t.shape)} of {t.dtype}")
+    return t.data_ptr()
+
+
+def _run(name, device, stream, *args):
+    """One C call on `stream` (default: the device's current one), with `device` current."""
+    torch = _torch()
+    fn = getattr(_capi.lib(), name)
+    st = _stream_ptr(stream, device)
+    if torch.cuda.current_device() == device.index:
+        _capi.check(fn(*args, st), name)
+    else:
+        with torch.cuda.device(device):
+            _capi.check(fn(*args, st), name)
+
+
+def _scratch(workspace, nbytes, device):
+    if workspace is None:
+        workspace = _torch().empty(max(nbytes, 1), dtype=_torch().uint8, device=device)
+    _dev(workspace, "workspace")
+    if workspace.device != device:
+        raise ValueError(f"workspace is on {workspace.device}, not on {device}")
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
+
+
+def _score(score):
+    if score not in SCORES:
+        raise ValueError(f"score must be one of {sorted(SCORES)}")
+    return SCORES[score]
+
+
+def _matrix(t, name, where):
+    _dev(t, name)
+    if t.dim() != 2:
+        raise ValueError(f"{where}: {name} must have two dimensions")
+    return t.shape
+
+
+def route_experts(logits, k: int, bias=None, score: str = "softmax", groups: int = 1,
+                  top_groups: int = 1, group_top: int = 1, renormalize: bool = True,
+                  scale: float = 1.0, experts=None, weights=None, scores=None,
+                  want_scores: bool = False, stream=None):
+    """Route tokens to experts (``sfn_route_experts`` in include/sfn.h).
+
+    logits [T, E] float32 or bf16, bias float32 [E] or None.  Returns (experts
+    int32 [T, k] in descending order of their selection scores, -1 for an empty
+    slot; weights float32 [T, k]; scores float32 [T, E], or None unless
+    ``scores`` or ``want_scores`` is given)."""
+    torch = _torch()
+    where = "route_experts"
+    T, E = _matrix(logits, "logits", where)
+    dev = logits.device
+    elt, kind = _elt(logits.dtype), _score(score)
+    bptr = None if bias is None else _arg(bias, "bias", where, dev, (E,), (torch.float32,))
+    if experts is None:
+        experts = torch.empty((T, max(k, 0)), dtype=torch.int32, device=dev)
+    if weights is None:
+        weights = torch.empty((T, max(k, 0)), dtype=torch.float32, device=dev)
+    if scores is None and want_scores:
+        scores = torch.empty((T, E), dtype=torch.float32, device=dev)
+    eptr = _arg(experts, "experts", where, dev, (T, max(k, 0)), (torch.int32,))
+    wptr = _arg(weights, "weights", where, dev, (T, max(k, 0)), (torch.float32,))
+    sptr = None if scores is None else _arg(scores, "scores", where, dev, (T, E),
+                                            (torch.float32,))
+    _run("sfn_route_experts", dev, stream, logits.data_ptr(), elt, bptr, eptr, wptr, sptr, T, E,
+         k, kind, groups, top_groups, group_top, int(bool(renormalize)), float(scale))
+    return experts, weights, scores
+
+
+def route_experts_backward(logits, experts, dweights, dscores=None, score: str = "softmax",
+                           renormalize: bool = True, scale: float = 1.0, dlogits=None,
+                           stream=None):
+    """Gradient of ``route_experts`` with respect to its logits, in their dtype,
+    for dweights float32 [T, k] and, optionally, dscores float32 [T, E]."""
+    torch = _torch()
+    where = "route_experts_backward"
+    T, E = _matrix(logits, "logits", where)
+    dev = logits.device
+    elt, kind = _elt(logits.dtype), _score(score)
+    _, k = _matrix(experts, "experts", where)
+    eptr = _arg(experts, "experts", where, dev, (T, k), (torch.int32,))
+    wptr = _arg(dweights, "dweights", where, dev, (T, k), (torch.float32,))
+    sptr = None if dscores is None else _arg(dscores, "dscores", where, dev, (T, E),
+                                             (torch.float32,))
+    if dlogits is None:
+        dlogits = torch.empty_like(logits)
+    lptr = _arg(dlogits, "dlogits", where, dev, (T, E), (logits.dtype,))
+    _run("sfn_route_experts_backward", dev, stream, logits.data_ptr(), elt, eptr, wptr, sptr,
+         lptr, T, E, k, kind, int(bool(renormalize)), float(scale))
+    return dlogits
+
+
+def quantize_rows_i8(x, q=None, scale=None, stream=None):
+    """8-bit quantisation of the rows of x (float32 or bf16, [..., K]; any
+    leading dimensions, so that [E, N, K] weights go in one call).  Returns (q
+    int8 [..., K], scale float32 [...])."""
+    torch = _torch()
+    where = "quantize_rows_i8"
+    _dev(x, "x")
+    if x.dim() < 1:
+        raise ValueError(f"{where}: x must have a dimension")
+    dev, lead, K = x.device, x.shape[:-1], x.shape[-1]
+    if q is None:
+        q = torch.empty(x.shape, dtype=torch.int8, device=dev)
+    if scale is None:
+        scale = torch.empty(lead, dtype=torch.float32, device=dev)
+    qptr = _arg(q, "q", where, dev, x.shape, (torch.int8,))
+    sptr = _arg(scale, "scale", where, dev, lead, (torch.float32,))
+    _run("sfn_quantize_rows_i8", dev, stream, x.data_ptr(), _elt(x.dtype), qptr, sptr,
+         scale.numel(), K)
+    return q, scale
+
+
+def matmul_i8(xq, x_scale, wq, w_scale, out=None, out_dtype=None, stream=None):
+    """y[t][n] = x_scale[t] w_scale[n] sum_k xq[t][k] wq[n][k]: int8 xq [T, K]
+    and wq [N, K], float32 scales [T] and [N].  y [T, N] in out_dtype (bf16
+    unless given) or as ``out``."""
+    torch = _torch()
+    where = "matmul_i8"
+    T, K = _matrix(xq, "xq", where)
+    N = _matrix(wq, "wq", where)[0]
+    dev = xq.device
+    if out is None:
+        out = torch.empty((T, N), dtype=out_dtype or torch.bfloat16, device=dev)
+    ptrs = [_arg(xq, "xq", where, dev, (T, K), (torch.int8,)),
+            _arg(x_scale, "x_scale", where, dev, (T,), (torch.float32,)),
+            _arg(wq, "wq", where, dev, (N, K), (torch.int8,)),
+            _arg(w_scale, "w_scale", where, dev, (N,), (torch.float32,)),
+            _arg(out, "out", where, dev, (T, N), (out_dtype or out.dtype,))]
+    _run("sfn_matmul_i8", dev, stream, *ptrs, _elt(out.dtype), T, N, K)
+    return out
+
+
+def linear_i8_workspace_bytes(T: int, K: int) -> int:
+    return int(_capi.lib().sfn_linear_i8_workspace_bytes(T, K))
+
+
+def linear_i8(x, wq, w_scale, out=None, out_dtype=None, workspace=None, stream=None):
+    """x [T, K] (float32 or bf16), quantised row by row, times the int8 weight
+    wq [N, K] with its scales [N].  y [T, N] in out_dtype (x's unless given) or
+    as ``out``."""
+    torch = _torch()
+    where = "linear_i8"
+    T, K = _matrix(x, "x", where)
+    N = _matrix(wq, "wq", where)[0]
+    dev = x.device
+    if out is None:
+        out = torch.empty((T, N), dtype=out_dtype or x.dtype, device=dev)
+    wptr = _arg(wq, "wq", where, dev, (N, K), (torch.int8,))
+    sptr = _arg(w_scale, "w_scale", where, dev, (N,), (torch.float32,))
+    yptr = _arg(out, "out", where, dev, (T, N), (out_dtype or out.dtype,))
+    ws, nbytes, keep = _scratch(workspace, linear_i8_workspace_bytes(T, K), dev)
+    _run("sfn_linear_i8", dev, stream, x.data_ptr(), _elt(x.dtype), wptr, sptr, yptr,
+         _elt(out.dtype), T, N, K, ws, nbytes)
+    _used_on(keep, workspace, stream)
+    return out
+
+
+def _used_on(scratch, given, stream):
+    """Scratch taken here must not be reused by the allocator before `stream` is done."""
+    if given is None and stream is not None:
+        scratch.record_stream(stream)
+
+
+def experts_i8_workspace_bytes(T: int, E: int, k: int, d: int, f: int) -> int:
+    return int(_capi.lib().sfn_experts_i8_workspace_bytes(T, E, k, d, f))
+
+
+def experts_i8_forward(x, experts, weights, Wg, sg, Wu, su, Wd, sd, y=None, workspace=None,
+                       stream=None):
+    """y_t = sum_i weights[t][i] FFN_e(x_t), e = experts[t][i], with every
+    product in 8-bit integers (``sfn_experts_i8_forward`` in include/sfn.h).
+
+    x bf16 [T, d]; experts int32, weights float32 [T, k] from
+    ``route_experts``; Wg, Wu int8 [E, f, d] with scales [E, f], Wd int8
+    [E, d, f] with scales [E, d] from ``quantize_rows_i8``.  Returns y bf16
+    [T, d]."""
+    torch = _torch()
+    where = "experts_i8_forward"
+    T, d = _matrix(x, "x", where)
+    _, k = _matrix(experts, "experts", where)
+    dev = x.device
+    _dev(Wg, "Wg")
+    if Wg.dim() != 3:
+        raise ValueError(f"{where}: Wg must be [E, f, d]")
+    E, f = Wg.shape[0], Wg.shape[1]
+    if y is None:
+        y = torch.empty((T, d), dtype=torch.bfloat16, device=dev)
+    i8, f32, bf16 = (torch.int8,), (torch.float32,), (torch.bfloat16,)
+    ptrs = [_arg(x, "x", where, dev, (T, d), bf16),
+            _arg(experts, "experts", where, dev, (T, k), (torch.int32,)),
+            _arg(weights, "weights", where, dev, (T, k), f32),
+            _arg(Wg, "Wg", where, dev, (E, f, d), i8), _arg(sg, "sg", where, dev, (E, f), f32),
+            _arg(Wu, "Wu", where, dev, (E, f, d), i8), _arg(su, "su", where, dev, (E, f), f32),
+            _arg(Wd, "Wd", where, dev, (E, d, f), i8), _arg(sd, "sd", where, dev, (E, d), f32),
+            _arg(y, "y", where, dev, (T, d), bf16)]
+    ws, nbytes, keep = _scratch(workspace, experts_i8_workspace_bytes(T, E, k, d, f), dev)
+    _run("sfn_experts_i8_forward", dev, stream, *ptrs, T, E, k, d, f, ws, nbytes)
+    _used_on(keep, workspace, stream)
+    return y

@@ -24,6 +24,9 @@ SFN_PATH_TENSOR = 2
 SFN_DTYPE_BF16 = 0
 SFN_DTYPE_F32 = 1
 
+SFN_SCORE_SOFTMAX = 0
+SFN_SCORE_SIGMOID = 1
+
 # Every function declared in include/sfn.h, with (restype, argtypes).
 _vp, _i64, _ci, _sz = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_size_t
 _FWD = [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _ci, _ci, _ci, _ci, _ci]
@@ -50,6 +53,16 @@ SIGNATURES = {
     "sfn_sparse_ffn_backward": (_ci, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, ctypes.c_float, _vp, _vp,
                                       _vp, _vp, _vp, _vp, _vp, _i64, _ci, _ci, _ci, _ci, _ci,
                                       _vp, _sz, _vp]),
+    "sfn_route_experts": (_ci, [_vp, _ci, _vp, _vp, _vp, _vp, _i64, _ci, _ci, _ci, _ci, _ci, _ci,
+                                _ci, ctypes.c_float, _vp]),
+    "sfn_route_experts_backward": (_ci, [_vp, _ci, _vp, _vp, _vp, _vp, _i64, _ci, _ci, _ci, _ci,
+                                         ctypes.c_float, _vp]),
+    "sfn_quantize_rows_i8": (_ci, [_vp, _ci, _vp, _vp, _i64, _ci, _vp]),
+    "sfn_matmul_i8": (_ci, [_vp, _vp, _vp, _vp, _vp, _ci, _i64, _ci, _ci, _vp]),
+    "sfn_linear_i8_workspace_bytes": (_sz, [_i64, _ci]),
+    "sfn_linear_i8": (_ci, [_vp, _ci, _vp, _vp, _vp, _ci, _i64, _ci, _ci, _vp, _sz, _vp]),
+    "sfn_experts_i8_workspace_bytes": (_sz, [_i64, _ci, _ci, _ci, _ci]),
+    "sfn_experts_i8_forward": (_ci, [_vp] * 10 + [_i64, _ci, _ci, _ci, _ci, _vp, _sz, _vp]),
     "sfn_timing_begin": (_ci, []),
     "sfn_device_errors": (_ci, [_vp, _ci]),
     "sfn_debug_wait_timeout": (_ci, [ctypes.c_longlong, _vp, _vp]),

@@ -10,6 +10,7 @@
 #include <utility>
 #include <vector>
 
+#include "experts.cuh"
 #include "sfn_internal.cuh"
 
 namespace sfn {
@@ -781,6 +782,215 @@ sfn_status sfn_sparse_ffn_backward(const void *x, const void *A, const void *B, 
   return cuda_status(e);
 }
 
+// ------------------------------------------------------------------ experts
+namespace {
+constexpr int kMaxI8K = 131072;  // 127^2 K < 2^31
+
+bool dtype_ok(sfn_dtype d) { return d == SFN_DTYPE_BF16 || d == SFN_DTYPE_F32; }
+size_t elt_bytes(sfn_dtype d) { return d == SFN_DTYPE_BF16 ? 2 : 4; }
+
+sfn_status check_route(sfn_dtype dtype, int64_t T, int E, int k, sfn_score score, int groups,
+                       int top_groups, int group_top, float scale) {
+  if (T < 0 || E <= 0 || k <= 0 || k > E || groups <= 0 || top_groups <= 0 ||
+      top_groups > groups || E % groups != 0 || group_top < 1 || group_top > 2 ||
+      k > (int64_t)top_groups * (E / groups) || !std::isfinite(scale) || !dtype_ok(dtype) ||
+      (score != SFN_SCORE_SOFTMAX && score != SFN_SCORE_SIGMOID))
+    return SFN_ERR_INVALID_VALUE;
+  if (E > kMaxExperts || k > kMaxExpertsPerTok || groups > kMaxGroups) return SFN_ERR_UNSUPPORTED;
+  return SFN_OK;
+}
+
+sfn_status check_i8(int64_t T, int N, int K) {
+  if (T < 0 || N <= 0 || K <= 0) return SFN_ERR_INVALID_VALUE;
+  if (K % 16 != 0) return SFN_ERR_MISALIGNED;
+  if (K > kMaxI8K || N > kMaxDi || T > 0x7fffffffLL ||
+      (T + 15) / 16 * ((N + 127) / 128) > 0x7fffffffLL)
+    return SFN_ERR_UNSUPPORTED;
+  return SFN_OK;
+}
+
+sfn_status check_experts(int64_t T, int E, int k, int d, int f) {
+  if (T < 0 || E <= 0 || k <= 0 || d <= 0 || f <= 0) return SFN_ERR_INVALID_VALUE;
+  if (d % 16 != 0 || f % 16 != 0) return SFN_ERR_MISALIGNED;
+  if (E > kMaxExperts || k > kMaxExpertsPerTok || T > 0x7fffffffLL / k) return SFN_ERR_UNSUPPORTED;
+  for (const int n : {d, f}) {
+    const sfn_status s0 = check_i8(T * k + 16 * (int64_t)E, n, n == d ? f : d);
+    if (s0 != SFN_OK) return s0;
+    if ((int64_t)E * n > 0x7fffffffLL) return SFN_ERR_UNSUPPORTED;
+  }
+  return SFN_OK;
+}
+
+size_t linear_scale_offset(int64_t T, int K) { return align_up((size_t)T * K, 256); }
+}  // namespace
+
+sfn_status sfn_route_experts(const void *logits, sfn_dtype dtype, const float *bias,
+                             int32_t *experts, float *weights, float *scores, int64_t T, int E,
+                             int k, sfn_score score, int groups, int top_groups, int group_top,
+                             int renormalize, float scale, sfn_stream_t stream) {
+  const sfn_status s0 = check_route(dtype, T, E, k, score, groups, top_groups, group_top, scale);
+  if (s0 != SFN_OK) return s0;
+  if (T == 0) return SFN_OK;
+  if (!logits || !experts || !weights) return SFN_ERR_INVALID_VALUE;
+  if (!aligned(logits, elt_bytes(dtype)) || !aligned(bias, 4) || !aligned(experts, 4) ||
+      !aligned(weights, 4) || !aligned(scores, 4))
+    return SFN_ERR_MISALIGNED;
+  DeviceInfo dev;
+  if (!device_info(&dev)) return SFN_ERR_CUDA;
+  const RouteShape s{T, E, k, dtype == SFN_DTYPE_BF16, score == SFN_SCORE_SIGMOID,
+                     groups, top_groups, group_top, renormalize != 0, scale};
+  cudaStream_t st = (cudaStream_t)stream;
+  return cuda_status(timed(SFN_STAGE_ROUTE, st, [&] {
+    return launch_route(s, logits, bias, experts, weights, scores, dev.num_sms, st);
+  }));
+}
+
+sfn_status sfn_route_experts_backward(const void *logits, sfn_dtype dtype,
+                                      const int32_t *experts, const float *dweights,
+                                      const float *dscores, void *dlogits, int64_t T, int E,
+                                      int k, sfn_score score, int renormalize, float scale,
+                                      sfn_stream_t stream) {
+  const sfn_status s0 = check_route(dtype, T, E, k, score, 1, 1, 1, scale);
+  if (s0 != SFN_OK) return s0;
+  if (T == 0) return SFN_OK;
+  if (!logits || !experts || !dweights || !dlogits) return SFN_ERR_INVALID_VALUE;
+  if (!aligned(logits, elt_bytes(dtype)) || !aligned(dlogits, elt_bytes(dtype)) ||
+      !aligned(experts, 4) || !aligned(dweights, 4) || !aligned(dscores, 4))
+    return SFN_ERR_MISALIGNED;
+  DeviceInfo dev;
+  if (!device_info(&dev)) return SFN_ERR_CUDA;
+  const RouteShape s{T, E, k, dtype == SFN_DTYPE_BF16, score == SFN_SCORE_SIGMOID,
+                     1, 1, 1, renormalize != 0, scale};
+  cudaStream_t st = (cudaStream_t)stream;
+  return cuda_status(timed(SFN_STAGE_ROUTE, st, [&] {
+    return launch_route_backward(s, logits, experts, dweights, dscores, dlogits, dev.num_sms, st);
+  }));
+}
+
+sfn_status sfn_quantize_rows_i8(const void *x, sfn_dtype dtype, int8_t *q, float *scale,
+                                int64_t T, int K, sfn_stream_t stream) {
+  if (!dtype_ok(dtype)) return SFN_ERR_INVALID_VALUE;
+  const sfn_status s0 = check_i8(T, 1, K);
+  if (s0 != SFN_OK) return s0;
+  if (T == 0) return SFN_OK;
+  if (!x || !q || !scale) return SFN_ERR_INVALID_VALUE;
+  if (!aligned(x, 16) || !aligned(q, 16) || !aligned(scale, 4)) return SFN_ERR_MISALIGNED;
+  DeviceInfo dev;
+  if (!device_info(&dev)) return SFN_ERR_CUDA;
+  cudaStream_t st = (cudaStream_t)stream;
+  return cuda_status(timed(SFN_STAGE_I8_ROWS, st, [&] {
+    return launch_quantize_rows(x, dtype == SFN_DTYPE_BF16, q, scale, T, K, dev.num_sms, st);
+  }));
+}
+
+sfn_status sfn_matmul_i8(const int8_t *xq, const float *x_scale, const int8_t *wq,
+                         const float *w_scale, void *y, sfn_dtype y_dtype, int64_t T, int N,
+                         int K, sfn_stream_t stream) {
+  if (!dtype_ok(y_dtype)) return SFN_ERR_INVALID_VALUE;
+  const sfn_status s0 = check_i8(T, N, K);
+  if (s0 != SFN_OK) return s0;
+  if (T == 0) return SFN_OK;
+  if (!xq || !x_scale || !wq || !w_scale || !y) return SFN_ERR_INVALID_VALUE;
+  if (!aligned(xq, 16) || !aligned(wq, 16) || !aligned(y, 16) || !aligned(x_scale, 4) ||
+      !aligned(w_scale, 4))
+    return SFN_ERR_MISALIGNED;
+  DeviceInfo dev;
+  if (!device_info(&dev)) return SFN_ERR_CUDA;
+  cudaStream_t st = (cudaStream_t)stream;
+  const I8Shape s{T, N, K, y_dtype == SFN_DTYPE_BF16};
+  return cuda_status(timed(SFN_STAGE_I8_PRODUCT, st, [&] {
+    return launch_i8_gemm(s, dev, xq, x_scale, wq, w_scale, y, st);
+  }));
+}
+
+size_t sfn_linear_i8_workspace_bytes(int64_t T, int K) {
+  if (T == 0 || check_i8(T, 1, K) != SFN_OK) return 0;
+  return align_up(linear_scale_offset(T, K) + (size_t)T * sizeof(float), 256);
+}
+
+sfn_status sfn_linear_i8(const void *x, sfn_dtype x_dtype, const int8_t *wq,
+                         const float *w_scale, void *y, sfn_dtype y_dtype, int64_t T, int N,
+                         int K, void *ws, size_t ws_bytes, sfn_stream_t stream) {
+  if (!dtype_ok(x_dtype) || !dtype_ok(y_dtype)) return SFN_ERR_INVALID_VALUE;
+  const sfn_status s0 = check_i8(T, N, K);
+  if (s0 != SFN_OK) return s0;
+  if (T == 0) return SFN_OK;
+  if (!x || !wq || !w_scale || !y) return SFN_ERR_INVALID_VALUE;
+  if (!aligned(x, 16) || !aligned(wq, 16) || !aligned(y, 16) || !aligned(w_scale, 4))
+    return SFN_ERR_MISALIGNED;
+  if (ws == nullptr || !aligned(ws, 256) || ws_bytes < sfn_linear_i8_workspace_bytes(T, K))
+    return SFN_ERR_WORKSPACE;
+  DeviceInfo dev;
+  if (!device_info(&dev)) return SFN_ERR_CUDA;
+  cudaStream_t st = (cudaStream_t)stream;
+  int8_t *xq = static_cast<int8_t *>(ws);
+  float *sx = reinterpret_cast<float *>(static_cast<char *>(ws) + linear_scale_offset(T, K));
+  const I8Shape s{T, N, K, y_dtype == SFN_DTYPE_BF16};
+  cudaError_t e = timed(SFN_STAGE_I8_ROWS, st, [&] {
+    return launch_quantize_rows(x, x_dtype == SFN_DTYPE_BF16, xq, sx, T, K, dev.num_sms, st);
+  });
+  if (e == cudaSuccess)
+    e = timed(SFN_STAGE_I8_PRODUCT, st,
+              [&] { return launch_i8_gemm(s, dev, xq, sx, wq, w_scale, y, st); });
+  return cuda_status(e);
+}
+
+size_t sfn_experts_i8_workspace_bytes(int64_t T, int E, int k, int d, int f) {
+  if (T == 0 || check_experts(T, E, k, d, f) != SFN_OK) return 0;
+  return plan_experts(ExpertShape{T, E, k, d, f}).total;
+}
+
+sfn_status sfn_experts_i8_forward(const void *x, const int32_t *experts, const float *weights,
+                                  const int8_t *Wg, const float *sg, const int8_t *Wu,
+                                  const float *su, const int8_t *Wd, const float *sd, void *y,
+                                  int64_t T, int E, int k, int d, int f, void *ws,
+                                  size_t ws_bytes, sfn_stream_t stream) {
+  const sfn_status s0 = check_experts(T, E, k, d, f);
+  if (s0 != SFN_OK) return s0;
+  if (T == 0) return SFN_OK;
+  if (!x || !experts || !weights || !Wg || !sg || !Wu || !su || !Wd || !sd || !y)
+    return SFN_ERR_INVALID_VALUE;
+  for (const void *q : {x, (const void *)Wg, (const void *)Wu, (const void *)Wd, (const void *)y})
+    if (!aligned(q, 16)) return SFN_ERR_MISALIGNED;
+  for (const void *q : {(const void *)experts, (const void *)weights, (const void *)sg,
+                        (const void *)su, (const void *)sd})
+    if (!aligned(q, 4)) return SFN_ERR_MISALIGNED;
+  const ExpertShape s{T, E, k, d, f};
+  const ExpertPlan p = plan_experts(s);
+  if (ws == nullptr || !aligned(ws, 256) || ws_bytes < p.total) return SFN_ERR_WORKSPACE;
+  DeviceInfo dev;
+  if (!device_info(&dev)) return SFN_ERR_CUDA;
+  cudaStream_t st = (cudaStream_t)stream;
+  char *w = static_cast<char *>(ws);
+  int32_t *offsets = reinterpret_cast<int32_t *>(w + p.off_offsets);
+  int32_t *pos = reinterpret_cast<int32_t *>(w + p.off_pos);
+  int8_t *xq = reinterpret_cast<int8_t *>(w + p.off_xq);
+  float *sx = reinterpret_cast<float *>(w + p.off_sx);
+  uint16_t *h = reinterpret_cast<uint16_t *>(w + p.off_h);
+  int8_t *hq = reinterpret_cast<int8_t *>(w + p.off_hq);
+  float *sh = reinterpret_cast<float *>(w + p.off_sh);
+  float *o = reinterpret_cast<float *>(w + p.off_o);
+  cudaError_t e = cudaSuccess;
+  auto step = [&](int stage, auto &&launch) {
+    if (e == cudaSuccess) e = timed(stage, st, launch);
+  };
+  step(SFN_STAGE_I8_ROWS,
+       [&] { return launch_expert_plan(s, experts, offsets, pos, dev.err, st); });
+  step(SFN_STAGE_I8_ROWS,
+       [&] { return launch_quantize_gather(s, x, pos, xq, sx, dev.num_sms, st); });
+  step(SFN_STAGE_I8_PRODUCT, [&] {
+    return launch_i8_experts_gateup(s, dev, offsets, xq, sx, Wg, sg, Wu, su, h, st);
+  });
+  step(SFN_STAGE_I8_ROWS,
+       [&] { return launch_quantize_expert_rows(s, h, offsets, hq, sh, dev.num_sms, st); });
+  step(SFN_STAGE_I8_PRODUCT,
+       [&] { return launch_i8_experts_down(s, dev, offsets, hq, sh, Wd, sd, o, st); });
+  step(SFN_STAGE_I8_ROWS, [&] {
+    return launch_expert_combine(s, o, pos, weights, static_cast<uint16_t *>(y), st);
+  });
+  return cuda_status(e);
+}
+
 const char *sfn_stage_name(int stage) {
   switch (stage) {
     case SFN_STAGE_PRED_H: return "pred_h";
@@ -791,11 +1001,14 @@ const char *sfn_stage_name(int stage) {
     case SFN_STAGE_TC_LOGITS_TOPK: return "tc_logits_topk";
     case SFN_STAGE_TC_GATEUP: return "tc_gateup";
     case SFN_STAGE_TC_DOWN: return "tc_down";
+    case SFN_STAGE_ROUTE: return "route";
     case SFN_STAGE_DENSE4X_GATEUP: return "dense4x_gateup";
     case SFN_STAGE_BWD_TAU: return "bwd_tau";
     case SFN_STAGE_BWD_ELEM: return "bwd_elem";
     case SFN_STAGE_BWD_GEMM: return "bwd_gemm";
     case SFN_STAGE_BANK_TOPK: return "bank_topk";
+    case SFN_STAGE_I8_PRODUCT: return "i8_product";
+    case SFN_STAGE_I8_ROWS: return "i8_rows";
   }
   return "unused";
 }

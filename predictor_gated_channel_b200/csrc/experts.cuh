@@ -1,0 +1,85 @@
+// experts.cuh -- host launcher declarations of the expert operators: routing
+// to experts (route.cu), the product in 8-bit integers (quant_i8.cu,
+// tc_i8.cu) and the experts' SwiGLU products (experts.cu).
+#pragma once
+
+#include "sfn_internal.cuh"
+
+namespace sfn {
+
+// ------------------------------------------------------------------ routing
+constexpr int kMaxExperts = 1024;    // V = 32 values per lane of a row's warp
+constexpr int kMaxExpertsPerTok = 32;  // lane i of the row's warp holds slot i
+constexpr int kMaxGroups = 32;       // at least one lane per group
+
+struct RouteShape {
+  int64_t T;
+  int E, k;
+  bool bf16;     // logits (and dlogits) in bf16, else float32
+  bool sigmoid;  // scores: sigmoid, else softmax
+  int groups, top_groups, group_top;
+  bool renorm;
+  float scale;
+};
+cudaError_t launch_route(const RouteShape &s, const void *logits, const float *bias,
+                         int32_t *experts, float *weights, float *scores, int num_sms,
+                         cudaStream_t st);
+cudaError_t launch_route_backward(const RouteShape &s, const void *logits,
+                                  const int32_t *experts, const float *dweights,
+                                  const float *dscores, void *dlogits, int num_sms,
+                                  cudaStream_t st);
+
+// ------------------------------------------------------- 8-bit integer product
+// Row-wise symmetric quantisation: scale = max |x| / 127, q = rint(127 x / max |x|).
+cudaError_t launch_quantize_rows(const void *x, bool bf16, int8_t *q, float *scale, int64_t T,
+                                 int K, int num_sms, cudaStream_t st);
+
+// y[t][n] = sx[t] sw[n] sum_k xq[t][k] wq[n][k].
+struct I8Shape {
+  int64_t T;
+  int N, K;
+  bool out_bf16;
+};
+cudaError_t launch_i8_gemm(const I8Shape &s, const DeviceInfo &dev, const int8_t *xq,
+                           const float *sx, const int8_t *wq, const float *sw, void *y,
+                           cudaStream_t st);
+
+// ------------------------------------------------------------- expert products
+struct ExpertShape {
+  int64_t T;
+  int E, k, d, f;
+  int64_t slots() const { return T * k; }
+};
+// Rows grouped by expert: expert e's rows are [offsets[e], offsets[e + 1]).
+// h[row][f] = bf16(silu(g) u), g and u the int8 products with Wg, Wu.
+cudaError_t launch_i8_experts_gateup(const ExpertShape &s, const DeviceInfo &dev,
+                                     const int32_t *offsets, const int8_t *xq, const float *sx,
+                                     const int8_t *Wg, const float *sg, const int8_t *Wu,
+                                     const float *su, uint16_t *h, cudaStream_t st);
+// o[row][d] float32, the int8 product with Wd.
+cudaError_t launch_i8_experts_down(const ExpertShape &s, const DeviceInfo &dev,
+                                   const int32_t *offsets, const int8_t *hq, const float *sh,
+                                   const int8_t *Wd, const float *sd, float *o,
+                                   cudaStream_t st);
+
+// Scratch of the experts' products.
+struct ExpertPlan {
+  size_t off_offsets, off_pos, off_xq, off_sx, off_h, off_hq, off_sh, off_o, total;
+};
+ExpertPlan plan_experts(const ExpertShape &s);
+
+// offsets[E + 1] and, for slot t * k + i, its row pos (-1: empty slot).
+cudaError_t launch_expert_plan(const ExpertShape &s, const int32_t *experts, int32_t *offsets,
+                               int32_t *pos, unsigned *err, cudaStream_t st);
+// Quantise x once per token and copy it to the rows of the token's slots.
+cudaError_t launch_quantize_gather(const ExpertShape &s, const void *x, const int32_t *pos,
+                                   int8_t *xq, float *sx, int num_sms, cudaStream_t st);
+// Quantise the first offsets[E] rows of h.
+cudaError_t launch_quantize_expert_rows(const ExpertShape &s, const uint16_t *h,
+                                        const int32_t *offsets, int8_t *hq, float *sh,
+                                        int num_sms, cudaStream_t st);
+// y[t] = sum_i weights[t][i] o[pos[t][i]].
+cudaError_t launch_expert_combine(const ExpertShape &s, const float *o, const int32_t *pos,
+                                  const float *weights, uint16_t *y, cudaStream_t st);
+
+}  // namespace sfn
