@@ -268,27 +268,37 @@ def sparse_ffn_backward(x, A, B, Wg, Wu, Wd, dy, bank: int = 64, k: int = 16,
 SCORES = {"softmax": _capi.SFN_SCORE_SOFTMAX, "sigmoid": _capi.SFN_SCORE_SIGMOID}
 
 
-def _arg(t, name, where, device, shape, dtypes):
-    """A contiguous CUDA tensor on `device` of this shape and one of these dtypes."""
-    _dev(t, name)
+_fns = {}
+
+
+def _arg(t, name, where, device, shape, dtype):
+    """The pointer of a contiguous CUDA tensor on `device` of this shape and dtype."""
+    torch = _torch()
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or not t.is_contiguous():
+        _dev(t, name)
     if t.device != device:
         raise ValueError(f"{where}: {name} is on {t.device}, not on {device}")
-    if tuple(t.shape) != tuple(shape) or t.dtype not in dtypes:
-        raise ValueError(f"{where}: {name} must be {list(shape)} of "
-                         f"{' or '.join(str(d) for d in dtypes)}, not {list(t.shape)} of {t.dtype}")
+    if t.shape != shape or t.dtype is not dtype:
+        raise ValueError(f"{where}: {name} must be {list(shape)} of {dtype}, not "
+                         f"{list(t.shape)} of {t.dtype}")
     return t.data_ptr()
 
 
 def _run(name, device, stream, *args):
     """One C call on `stream` (default: the device's current one), with `device` current."""
     torch = _torch()
-    fn = getattr(_capi.lib(), name)
-    st = _stream_ptr(stream, device)
+    fn = _fns.get(name)
+    if fn is None:
+        fn = _fns[name] = getattr(_capi.lib(), name)
+    st = (torch._C._cuda_getCurrentRawStream(device.index) if stream is None
+          else stream.cuda_stream)
     if torch.cuda.current_device() == device.index:
-        _capi.check(fn(*args, st), name)
+        status = fn(*args, st)
     else:
         with torch.cuda.device(device):
-            _capi.check(fn(*args, st), name)
+            status = fn(*args, st)
+    if status:
+        _capi.check(status, name)
 
 
 def _scratch(workspace, nbytes, device):
@@ -307,7 +317,8 @@ def _score(score):
 
 
 def _matrix(t, name, where):
-    _dev(t, name)
+    if not isinstance(t, _torch().Tensor) or not t.is_cuda or not t.is_contiguous():
+        _dev(t, name)
     if t.dim() != 2:
         raise ValueError(f"{where}: {name} must have two dimensions")
     return t.shape
@@ -328,17 +339,17 @@ def route_experts(logits, k: int, bias=None, score: str = "softmax", groups: int
     T, E = _matrix(logits, "logits", where)
     dev = logits.device
     elt, kind = _elt(logits.dtype), _score(score)
-    bptr = None if bias is None else _arg(bias, "bias", where, dev, (E,), (torch.float32,))
+    bptr = None if bias is None else _arg(bias, "bias", where, dev, (E,), torch.float32)
     if experts is None:
         experts = torch.empty((T, max(k, 0)), dtype=torch.int32, device=dev)
     if weights is None:
         weights = torch.empty((T, max(k, 0)), dtype=torch.float32, device=dev)
     if scores is None and want_scores:
         scores = torch.empty((T, E), dtype=torch.float32, device=dev)
-    eptr = _arg(experts, "experts", where, dev, (T, max(k, 0)), (torch.int32,))
-    wptr = _arg(weights, "weights", where, dev, (T, max(k, 0)), (torch.float32,))
+    eptr = _arg(experts, "experts", where, dev, (T, max(k, 0)), torch.int32)
+    wptr = _arg(weights, "weights", where, dev, (T, max(k, 0)), torch.float32)
     sptr = None if scores is None else _arg(scores, "scores", where, dev, (T, E),
-                                            (torch.float32,))
+                                            torch.float32)
     _run("sfn_route_experts", dev, stream, logits.data_ptr(), elt, bptr, eptr, wptr, sptr, T, E,
          k, kind, groups, top_groups, group_top, int(bool(renormalize)), float(scale))
     return experts, weights, scores
@@ -355,13 +366,13 @@ def route_experts_backward(logits, experts, dweights, dscores=None, score: str =
     dev = logits.device
     elt, kind = _elt(logits.dtype), _score(score)
     _, k = _matrix(experts, "experts", where)
-    eptr = _arg(experts, "experts", where, dev, (T, k), (torch.int32,))
-    wptr = _arg(dweights, "dweights", where, dev, (T, k), (torch.float32,))
+    eptr = _arg(experts, "experts", where, dev, (T, k), torch.int32)
+    wptr = _arg(dweights, "dweights", where, dev, (T, k), torch.float32)
     sptr = None if dscores is None else _arg(dscores, "dscores", where, dev, (T, E),
-                                             (torch.float32,))
+                                             torch.float32)
     if dlogits is None:
         dlogits = torch.empty_like(logits)
-    lptr = _arg(dlogits, "dlogits", where, dev, (T, E), (logits.dtype,))
+    lptr = _arg(dlogits, "dlogits", where, dev, (T, E), logits.dtype)
     _run("sfn_route_experts_backward", dev, stream, logits.data_ptr(), elt, eptr, wptr, sptr,
          lptr, T, E, k, kind, int(bool(renormalize)), float(scale))
     return dlogits
@@ -381,8 +392,8 @@ def quantize_rows_i8(x, q=None, scale=None, stream=None):
         q = torch.empty(x.shape, dtype=torch.int8, device=dev)
     if scale is None:
         scale = torch.empty(lead, dtype=torch.float32, device=dev)
-    qptr = _arg(q, "q", where, dev, x.shape, (torch.int8,))
-    sptr = _arg(scale, "scale", where, dev, lead, (torch.float32,))
+    qptr = _arg(q, "q", where, dev, x.shape, torch.int8)
+    sptr = _arg(scale, "scale", where, dev, lead, torch.float32)
     _run("sfn_quantize_rows_i8", dev, stream, x.data_ptr(), _elt(x.dtype), qptr, sptr,
          scale.numel(), K)
     return q, scale
@@ -399,11 +410,11 @@ def matmul_i8(xq, x_scale, wq, w_scale, out=None, out_dtype=None, stream=None):
     dev = xq.device
     if out is None:
         out = torch.empty((T, N), dtype=out_dtype or torch.bfloat16, device=dev)
-    ptrs = [_arg(xq, "xq", where, dev, (T, K), (torch.int8,)),
-            _arg(x_scale, "x_scale", where, dev, (T,), (torch.float32,)),
-            _arg(wq, "wq", where, dev, (N, K), (torch.int8,)),
-            _arg(w_scale, "w_scale", where, dev, (N,), (torch.float32,)),
-            _arg(out, "out", where, dev, (T, N), (out_dtype or out.dtype,))]
+    ptrs = [_arg(xq, "xq", where, dev, (T, K), torch.int8),
+            _arg(x_scale, "x_scale", where, dev, (T,), torch.float32),
+            _arg(wq, "wq", where, dev, (N, K), torch.int8),
+            _arg(w_scale, "w_scale", where, dev, (N,), torch.float32),
+            _arg(out, "out", where, dev, (T, N), out_dtype or out.dtype)]
     _run("sfn_matmul_i8", dev, stream, *ptrs, _elt(out.dtype), T, N, K)
     return out
 
@@ -423,9 +434,9 @@ def linear_i8(x, wq, w_scale, out=None, out_dtype=None, workspace=None, stream=N
     dev = x.device
     if out is None:
         out = torch.empty((T, N), dtype=out_dtype or x.dtype, device=dev)
-    wptr = _arg(wq, "wq", where, dev, (N, K), (torch.int8,))
-    sptr = _arg(w_scale, "w_scale", where, dev, (N,), (torch.float32,))
-    yptr = _arg(out, "out", where, dev, (T, N), (out_dtype or out.dtype,))
+    wptr = _arg(wq, "wq", where, dev, (N, K), torch.int8)
+    sptr = _arg(w_scale, "w_scale", where, dev, (N,), torch.float32)
+    yptr = _arg(out, "out", where, dev, (T, N), out_dtype or out.dtype)
     ws, nbytes, keep = _scratch(workspace, linear_i8_workspace_bytes(T, K), dev)
     _run("sfn_linear_i8", dev, stream, x.data_ptr(), _elt(x.dtype), wptr, sptr, yptr,
          _elt(out.dtype), T, N, K, ws, nbytes)
@@ -463,9 +474,9 @@ def experts_i8_forward(x, experts, weights, Wg, sg, Wu, su, Wd, sd, y=None, work
     E, f = Wg.shape[0], Wg.shape[1]
     if y is None:
         y = torch.empty((T, d), dtype=torch.bfloat16, device=dev)
-    i8, f32, bf16 = (torch.int8,), (torch.float32,), (torch.bfloat16,)
+    i8, f32, bf16 = torch.int8, torch.float32, torch.bfloat16
     ptrs = [_arg(x, "x", where, dev, (T, d), bf16),
-            _arg(experts, "experts", where, dev, (T, k), (torch.int32,)),
+            _arg(experts, "experts", where, dev, (T, k), torch.int32),
             _arg(weights, "weights", where, dev, (T, k), f32),
             _arg(Wg, "Wg", where, dev, (E, f, d), i8), _arg(sg, "sg", where, dev, (E, f), f32),
             _arg(Wu, "Wu", where, dev, (E, f, d), i8), _arg(su, "su", where, dev, (E, f), f32),

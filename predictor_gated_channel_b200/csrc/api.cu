@@ -923,9 +923,13 @@ sfn_status sfn_linear_i8(const void *x, sfn_dtype x_dtype, const int8_t *wq,
   DeviceInfo dev;
   if (!device_info(&dev)) return SFN_ERR_CUDA;
   cudaStream_t st = (cudaStream_t)stream;
+  const I8Shape s{T, N, K, y_dtype == SFN_DTYPE_BF16};
+  if (linear_gemv_ok(s, dev.num_sms))
+    return cuda_status(timed(SFN_STAGE_I8_PRODUCT, st, [&] {
+      return launch_linear_gemv(s, x_dtype == SFN_DTYPE_BF16, dev, x, wq, w_scale, y, st);
+    }));
   int8_t *xq = static_cast<int8_t *>(ws);
   float *sx = reinterpret_cast<float *>(static_cast<char *>(ws) + linear_scale_offset(T, K));
-  const I8Shape s{T, N, K, y_dtype == SFN_DTYPE_BF16};
   cudaError_t e = timed(SFN_STAGE_I8_ROWS, st, [&] {
     return launch_quantize_rows(x, x_dtype == SFN_DTYPE_BF16, xq, sx, T, K, dev.num_sms, st);
   });
@@ -974,6 +978,16 @@ sfn_status sfn_experts_i8_forward(const void *x, const int32_t *experts, const f
   auto step = [&](int stage, auto &&launch) {
     if (e == cudaSuccess) e = timed(stage, st, launch);
   };
+  if (experts_gemv_ok(s, dev.num_sms)) {
+    step(SFN_STAGE_I8_PRODUCT, [&] {
+      return launch_experts_gemv_gateup(s, dev, x, experts, Wg, sg, Wu, su, h, st);
+    });
+    step(SFN_STAGE_I8_PRODUCT, [&] {
+      return launch_experts_gemv_down(s, dev, h, experts, weights, Wd, sd,
+                                      static_cast<uint16_t *>(y), st);
+    });
+    return cuda_status(e);
+  }
   step(SFN_STAGE_I8_ROWS,
        [&] { return launch_expert_plan(s, experts, offsets, pos, dev.err, st); });
   step(SFN_STAGE_I8_ROWS,

@@ -44,6 +44,14 @@ cudaError_t launch_i8_gemm(const I8Shape &s, const DeviceInfo &dev, const int8_t
                            const float *sx, const int8_t *wq, const float *sw, void *y,
                            cudaStream_t st);
 
+// For a few tokens: the quantisation and the product in one kernel that
+// streams the weight rows.
+constexpr int kGemvTokens = 4;
+bool linear_gemv_ok(const I8Shape &s, int num_sms);
+cudaError_t launch_linear_gemv(const I8Shape &s, bool x_bf16, const DeviceInfo &dev,
+                               const void *x, const int8_t *wq, const float *sw, void *y,
+                               cudaStream_t st);
+
 // ------------------------------------------------------------- expert products
 struct ExpertShape {
   int64_t T;
@@ -61,6 +69,19 @@ cudaError_t launch_i8_experts_down(const ExpertShape &s, const DeviceInfo &dev,
                                    const int32_t *offsets, const int8_t *hq, const float *sh,
                                    const int8_t *Wd, const float *sd, float *o,
                                    cudaStream_t st);
+
+// For a few slots (T k <= kGemvSlots): gate/up and down as streams of the
+// slots' weight rows, each slot on its own.  h is [T k][f] in slot order.
+constexpr int kGemvSlots = 32;
+bool experts_gemv_ok(const ExpertShape &s, int num_sms);
+cudaError_t launch_experts_gemv_gateup(const ExpertShape &s, const DeviceInfo &dev, const void *x,
+                                       const int32_t *experts, const int8_t *Wg, const float *sg,
+                                       const int8_t *Wu, const float *su, uint16_t *h,
+                                       cudaStream_t st);
+cudaError_t launch_experts_gemv_down(const ExpertShape &s, const DeviceInfo &dev,
+                                     const uint16_t *h, const int32_t *experts,
+                                     const float *weights, const int8_t *Wd, const float *sd,
+                                     uint16_t *y, cudaStream_t st);
 
 // Scratch of the experts' products.
 struct ExpertPlan {
