@@ -899,7 +899,7 @@ sfn_status sfn_matmul_i8(const int8_t *xq, const float *x_scale, const int8_t *w
   cudaStream_t st = (cudaStream_t)stream;
   const I8Shape s{T, N, K, y_dtype == SFN_DTYPE_BF16};
   return cuda_status(timed(SFN_STAGE_I8_PRODUCT, st, [&] {
-    return launch_i8_gemm(s, dev, xq, x_scale, wq, w_scale, y, st);
+    return launch_i8_gemm(s, dev, xq, x_scale, wq, w_scale, y, false, st);
   }));
 }
 
@@ -935,7 +935,7 @@ sfn_status sfn_linear_i8(const void *x, sfn_dtype x_dtype, const int8_t *wq,
   });
   if (e == cudaSuccess)
     e = timed(SFN_STAGE_I8_PRODUCT, st,
-              [&] { return launch_i8_gemm(s, dev, xq, sx, wq, w_scale, y, st); });
+              [&] { return launch_i8_gemm(s, dev, xq, sx, wq, w_scale, y, true, st); });
   return cuda_status(e);
 }
 

@@ -34,7 +34,9 @@ cudaError_t launch_route_backward(const RouteShape &s, const void *logits,
 cudaError_t launch_quantize_rows(const void *x, bool bf16, int8_t *q, float *scale, int64_t T,
                                  int K, int num_sms, cudaStream_t st);
 
-// y[t][n] = sx[t] sw[n] sum_k xq[t][k] wq[n][k].
+// y[t][n] = sx[t] sw[n] sum_k xq[t][k] wq[n][k].  weights_early: the kernel
+// launched before this one on the stream neither writes wq nor lets this one
+// start before all work ahead of it is complete.
 struct I8Shape {
   int64_t T;
   int N, K;
@@ -42,7 +44,7 @@ struct I8Shape {
 };
 cudaError_t launch_i8_gemm(const I8Shape &s, const DeviceInfo &dev, const int8_t *xq,
                            const float *sx, const int8_t *wq, const float *sw, void *y,
-                           cudaStream_t st);
+                           bool weights_early, cudaStream_t st);
 
 // For a few tokens: the quantisation and the product in one kernel that
 // streams the weight rows.

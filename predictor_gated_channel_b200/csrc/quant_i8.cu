@@ -19,7 +19,7 @@ namespace sfn {
 namespace {
 
 constexpr int kQuantWarps = 8;  // per block
-constexpr int kHeld = 4;        // 16-byte chunks a thread holds
+constexpr int kHeld = 8;        // 16-byte chunks a thread holds
 
 // Source rows -> destination rows of one launch.
 struct QuantParams {
@@ -34,7 +34,7 @@ struct QuantParams {
 };
 
 template <class Elt, int kRowWarps>
-__global__ void __launch_bounds__(32 * kQuantWarps) k_quantize_rows(const QuantParams p) {
+__global__ void __launch_bounds__(32 * kQuantWarps, 4) k_quantize_rows(const QuantParams p) {
   constexpr int kThreads = 32 * kRowWarps;       // per row
   constexpr int kRows = kQuantWarps / kRowWarps;  // per block
   __shared__ uint32_t part[kQuantWarps];
@@ -54,11 +54,10 @@ __global__ void __launch_bounds__(32 * kQuantWarps) k_quantize_rows(const QuantP
 #pragma unroll
     for (int i = 0; i < kHeld; ++i) {
       const int c = th + i * kThreads;
-      if (c < chunks) held[i] = src[c];
+      held[i] = c < chunks ? src[c] : make_uint4(0u, 0u, 0u, 0u);
     }
 #pragma unroll
-    for (int i = 0; i < kHeld; ++i)
-      if (th + i * kThreads < chunks) amax = max(amax, abs_bits_max<Elt>(held[i]));
+    for (int i = 0; i < kHeld; ++i) amax = max(amax, abs_bits_max<Elt>(held[i]));
     for (int c = th + kHeld * kThreads; c < chunks; c += kThreads)
       amax = max(amax, abs_bits_max<Elt>(src[c]));
     amax = __reduce_max_sync(kFull, amax);
@@ -71,28 +70,22 @@ __global__ void __launch_bounds__(32 * kQuantWarps) k_quantize_rows(const QuantP
     }
     const QuantScale qs(amax);
     if (!have) continue;
+    using Out = typename QuantOut<Elt>::type;
     const int copies = p.pos != nullptr ? p.copies : 1;
-    for (int i = 0; i < kHeld || th + i * kThreads < chunks; ++i) {
-      const int c = th + i * kThreads;
-      if (c >= chunks) break;
-      uint4 v;
-      if (i < kHeld) {
+    Out out[kHeld];
 #pragma unroll
-        for (int h = 0; h < kHeld; ++h)
-          if (h == i) v = held[h];
-      } else {
-        v = src[c];
-      }
-      const typename QuantOut<Elt>::type o = quantize_chunk<Elt>(v, qs);
-      for (int k = 0; k < copies; ++k) {
-        const int64_t d = p.pos != nullptr ? p.pos[r * copies + k] : r;
-        if (d >= 0)
-          reinterpret_cast<typename QuantOut<Elt>::type *>(p.q + d * p.K)[c] = o;
-      }
-    }
-    if (th < copies) {
-      const int64_t d = p.pos != nullptr ? p.pos[r * copies + th] : r;
-      if (d >= 0) p.scale[d] = qs.scale;
+    for (int i = 0; i < kHeld; ++i) out[i] = quantize_chunk<Elt>(held[i], qs);
+    for (int k = 0; k < copies; ++k) {
+      const int64_t d = p.pos != nullptr ? p.pos[r * copies + k] : r;
+      if (d < 0) continue;
+      Out *dst = reinterpret_cast<Out *>(p.q + d * p.K);
+#pragma unroll
+      for (int i = 0; i < kHeld; ++i)
+        if (th + i * kThreads < chunks) dst[th + i * kThreads] = out[i];
+#pragma unroll 1
+      for (int c = th + kHeld * kThreads; c < chunks; c += kThreads)
+        dst[c] = quantize_chunk<Elt>(src[c], qs);
+      if (th == 0) p.scale[d] = qs.scale;
     }
   }
 }
