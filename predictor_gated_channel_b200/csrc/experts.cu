@@ -9,19 +9,22 @@
 #include "experts.cuh"
 #include "quant_i8.cuh"
 
+#include <cuda_fp16.h>
+
 namespace sfn {
 namespace {
 
 constexpr int kPlanThreads = 1024;  // >= kMaxExperts: one thread per expert scans
-constexpr int kCombineThreads = 256;
+constexpr int kPlanBatch = 8;
+constexpr int kCombineThreads = 128;
 
 // Counting sort of the slots by expert, one block.  Where a slot lands among
 // its expert's rows depends on the order of the shared-memory atomics, but no
 // result does: rows are computed independently of one another, and the
 // combine reads each slot's row through pos.
 __global__ void __launch_bounds__(kPlanThreads)
-    k_expert_plan(const int32_t *experts, int32_t *offsets, int32_t *pos, int64_t slots, int E,
-                  unsigned *err) {
+    k_expert_plan(const int32_t *__restrict__ experts, int32_t *__restrict__ offsets,
+                  int32_t *__restrict__ pos, int64_t slots, int E, unsigned *err) {
   __shared__ int cursor[kMaxExperts];
   __shared__ int warp_sum[32];
   pdl_wait();
@@ -30,13 +33,28 @@ __global__ void __launch_bounds__(kPlanThreads)
   if (tid < E) cursor[tid] = 0;
   __syncthreads();
   bool bad = false;
-  for (int64_t i = tid; i < slots; i += kPlanThreads) {
-    const int e = experts[i];
+  // kPlanBatch loads at a time: one block's only way to hide their latency
+  auto each = [&](auto &&f) {
+    for (int64_t i0 = tid; i0 < slots; i0 += kPlanThreads * kPlanBatch) {
+      int e[kPlanBatch];
+#pragma unroll
+      for (int j = 0; j < kPlanBatch; ++j) {
+        const int64_t i = i0 + (int64_t)j * kPlanThreads;
+        e[j] = i < slots ? __ldg(experts + i) : -1;
+      }
+#pragma unroll
+      for (int j = 0; j < kPlanBatch; ++j) {
+        const int64_t i = i0 + (int64_t)j * kPlanThreads;
+        if (i < slots) f(i, e[j]);
+      }
+    }
+  };
+  each([&](int64_t, int e) {
     if (e >= 0 && e < E)
       atomicAdd(&cursor[e], 1);
     else
       bad |= e >= E;
-  }
+  });
   if (bad) report_error(err, kDevErrBounds);
   __syncthreads();
   const int count = tid < E ? cursor[tid] : 0;
@@ -56,36 +74,45 @@ __global__ void __launch_bounds__(kPlanThreads)
   }
   if (tid == 0) offsets[0] = 0;
   __syncthreads();
-  for (int64_t i = tid; i < slots; i += kPlanThreads) {
-    const int e = experts[i];
-    pos[i] = (e >= 0 && e < E) ? atomicAdd(&cursor[e], 1) : -1;
-  }
+  each([&](int64_t i, int e) { pos[i] = (e >= 0 && e < E) ? atomicAdd(&cursor[e], 1) : -1; });
 }
 
-// One block per token: float32 sum over the slots in slot order.
+// y_t = sum over the slots, in slot order and float32; a thread has 8 channels.
+// Bound by the reads of o; the loads of four slots are issued together.
 __global__ void __launch_bounds__(kCombineThreads)
-    k_expert_combine(const float *__restrict__ o, const int32_t *__restrict__ pos,
-                     const float *__restrict__ weights, uint16_t *__restrict__ y, int k, int d) {
+    k_expert_combine(const uint16_t *__restrict__ o, const uint8_t *__restrict__ exponents,
+                     const int32_t *__restrict__ pos, const int32_t *__restrict__ experts,
+                     const float *__restrict__ sh, const float *__restrict__ weights,
+                     uint16_t *__restrict__ y, int k, int d, float inv_unit) {
   pdl_wait();
   pdl_launch_dependents();
   const int64_t t = blockIdx.x;
-  for (int c = threadIdx.x * 4; c < d; c += kCombineThreads * 4) {
-    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int i = 0; i < k; ++i) {
-      const int r = pos[t * k + i];
-      if (r < 0) continue;
-      const float w = weights[t * k + i];
-      const float4 v = *reinterpret_cast<const float4 *>(o + (int64_t)r * d + c);
-      s.x += w * v.x;
-      s.y += w * v.y;
-      s.z += w * v.z;
-      s.w += w * v.w;
+  const int c = (blockIdx.y * kCombineThreads + threadIdx.x) * 8;
+  if (c >= d) return;
+  const int blocks = (d + 31) / 32;
+  float s[8] = {};
+#pragma unroll 4
+  for (int i = 0; i < k; ++i) {
+    const int64_t at = t * k + i;
+    const int r = pos[at];
+    if (r < 0) continue;
+    const uint4 v = ld_stream16(o + (int64_t)r * d + c);
+    const uint32_t eb = exponents[(int64_t)experts[at] * blocks + c / 32];
+    const float f = weights[at] * (sh[r] * inv_unit) * __uint_as_float(eb << 23);
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float2 h = __half22float2(*reinterpret_cast<const __half2 *>(&w[j]));
+      s[2 * j] += f * h.x;
+      s[2 * j + 1] += f * h.y;
     }
-    uint2 out;
-    out.x = (uint32_t)f32_to_bf16_bits(s.x) | ((uint32_t)f32_to_bf16_bits(s.y) << 16);
-    out.y = (uint32_t)f32_to_bf16_bits(s.z) | ((uint32_t)f32_to_bf16_bits(s.w) << 16);
-    *reinterpret_cast<uint2 *>(y + t * d + c) = out;
   }
+  uint32_t out[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    out[j] = (uint32_t)f32_to_bf16_bits(s[2 * j]) |
+             ((uint32_t)f32_to_bf16_bits(s[2 * j + 1]) << 16);
+  *reinterpret_cast<uint4 *>(y + t * d + c) = make_uint4(out[0], out[1], out[2], out[3]);
 }
 
 }  // namespace
@@ -106,7 +133,8 @@ ExpertPlan plan_experts(const ExpertShape &s) {
   p.off_h = take(R * s.f * 2);
   p.off_hq = take(R * s.f);
   p.off_sh = take(R * 4);
-  p.off_o = take(R * s.d * 4);
+  p.off_o = take(R * s.d * 2);
+  p.off_exp = take((size_t)s.E * ((s.d + 31) / 32));
   p.total = off;
   return p;
 }
@@ -118,11 +146,15 @@ cudaError_t launch_expert_plan(const ExpertShape &s, const int32_t *experts, int
                     s.slots(), s.E, err);
 }
 
-cudaError_t launch_expert_combine(const ExpertShape &s, const float *o, const int32_t *pos,
-                                  const float *weights, uint16_t *y, cudaStream_t st) {
+cudaError_t launch_expert_combine(const ExpertShape &s, const uint16_t *o,
+                                  const uint8_t *exponents, const int32_t *pos,
+                                  const int32_t *experts, const float *sh, const float *weights,
+                                  uint16_t *y, cudaStream_t st) {
+  const unsigned parts = (unsigned)((s.d + 8 * kCombineThreads - 1) / (8 * kCombineThreads));
   count_launches(1);
-  return launch_pdl(k_expert_combine, dim3((unsigned)s.T), dim3(kCombineThreads), 0, st, o, pos,
-                    weights, y, s.k, s.d);
+  return launch_pdl(k_expert_combine, dim3((unsigned)s.T, parts), dim3(kCombineThreads), 0, st, o,
+                    exponents, pos, experts, sh, weights, y, s.k, s.d,
+                    1.f / expert_out_unit(s.f));
 }
 
 }  // namespace sfn

@@ -19,8 +19,8 @@
 //   warp 0      TMA producer: 128-byte K slices (128-byte swizzle) of the
 //               weight tile(s) and of the rows into a ring of stages
 //   warp 1      allocates 512 TMEM columns; one thread issues the MMAs
-//   warps 2..9  epilogue, two per TMEM lane quadrant (32 channels): lane =
-//               channel, register = row; a store writes 32 neighbouring
+//   warps 2...  epilogue, two or four per TMEM lane quadrant (32 channels):
+//               lane = channel, register = row; a store writes 32 neighbouring
 //               channels of one row
 // in three forms:
 //   kOne    a CTA per tile, persistent over tiles
@@ -39,6 +39,7 @@
 #include "tc_util.cuh"
 
 #include <cudaTypedefs.h>
+#include <cuda_fp16.h>
 
 #include <type_traits>
 
@@ -46,14 +47,15 @@ namespace sfn {
 namespace {
 
 enum class Span { kOne, kPair, kSplit };
+// What the scaled product is stored as.  kBlockHalf: without the row's scale,
+// in fp16 with a power of two for each 32 channels (see block_scale).
+enum class Out { kF32, kBF16, kBlockHalf };
 
 constexpr int kTileN = 128;                    // output channels per CTA (UMMA M, half of a pair's)
 constexpr int kSliceK = 128;                   // K bytes per stage
 constexpr uint32_t kTileBytes = kTileN * kSliceK;
 constexpr int kTmemCols = 512;
 constexpr int kRaster = 16;                    // row tiles of a rasterisation group
-constexpr int kEpiWarps = 8;
-constexpr int kThreads = (2 + kEpiWarps) * 32;
 constexpr size_t kMaxDynSmem = 232448;
 constexpr int kMaxStages = 12;
 constexpr int kMaxSplit = 8;                   // CTAs of a split tile (portable cluster size)
@@ -73,6 +75,8 @@ struct I8Params {
   bool early;              // the weights and offsets are there before the previous kernel's end
   const float *sx, *sw, *sw2;
   void *out;               // [rows][n]
+  uint8_t *exponents;      // kBlockHalf: [groups][ceil(n / 32)]
+  float unit;              // kBlockHalf: a power of two, at most 1 / K
   unsigned *err;
 };
 
@@ -165,8 +169,10 @@ __device__ __forceinline__ uint32_t at_rank(const void *p, uint32_t rank) {
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_u32(p)), "r"(rank));
   return r;
 }
+// Relaxed: what the arrival tells is that TMEM was read (tc_fence_before
+// orders that); a release would wait for the thread's global stores too.
 __device__ __forceinline__ void arrive_at(uint32_t cluster_addr) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr)
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr)
                : "memory");
 }
 __device__ __forceinline__ int4 ld_cluster16(uint32_t cluster_addr) {
@@ -247,13 +253,49 @@ __device__ __forceinline__ uint16_t bf16_bits(float f) {
   return r;
 }
 
-template <bool kSwiGlu, bool kOutBf16, Span kSpan>
-__global__ void __launch_bounds__(kThreads, 1)
+// Epilogue warps: 16 where a wide SwiGLU tile takes all of TMEM, so that the
+// MMAs wait for half as long (64 experts of 4096 x 1792 with 512 rows each: 789
+// us against 851 with 8), else 8 (8 rows an expert: 235 us against 245 with 16).
+template <bool kSwiGlu, Span kSpan>
+constexpr int epi_warps() {
+  return kSwiGlu && kSpan == Span::kPair ? 16 : 8;
+}
+template <bool kSwiGlu, Span kSpan>
+constexpr int block_threads() {
+  return (2 + epi_warps<kSwiGlu, kSpan>()) * 32;
+}
+
+template <Out kOut>
+__device__ __forceinline__ auto out_value(float y) {
+  if constexpr (kOut == Out::kBF16)
+    return bf16_bits(y);
+  else
+    return y;
+}
+
+// The experts' outputs before their weighted sum: half the bytes of float32
+// (they are the largest traffic of a prefill), rounded to 11 bits, an eighth
+// of the step of the bf16 sum.  The accumulator times unit (<= 1 / K) is below
+// 127^2; times sw over its block's power of two, below 4 * 127^2 < 65504, so
+// nothing overflows, and a channel loses bits to the range only where its scale
+// is below 2^-10 of its block's largest.  The exponent of the largest finite
+// |sw| of this warp's 32 channels:
+__device__ __forceinline__ int block_exponent(float sw) {
+  const uint32_t bits = __float_as_uint(sw) & 0x7fffffffu;
+  const uint32_t most = __reduce_max_sync(kFull, bits < 0x7f800000u ? bits : 0u);
+  return min(max((int)(most >> 23), 1), 253);
+}
+
+template <bool kSwiGlu, Out kOut, Span kSpan>
+__global__ void __launch_bounds__((block_threads<kSwiGlu, kSpan>()), 1)
     k_i8_gemm(const __grid_constant__ CUtensorMap tX, const __grid_constant__ CUtensorMap tW,
               const __grid_constant__ CUtensorMap tW2, const I8Params p) {
   constexpr bool kPair = kSpan == Span::kPair, kSplit = kSpan == Span::kSplit;
   static_assert(!(kSplit && kSwiGlu), "the split form has the scaled product only");
   constexpr int kNumW = kSwiGlu ? 2 : 1;
+  constexpr int kEpiWarps = epi_warps<kSwiGlu, kSpan>(), kThreads = (2 + kEpiWarps) * 32;
+  constexpr int kEpiParts = kEpiWarps / 4;          // warps per TMEM lane quadrant
+  constexpr int kEpiChunks = 256 / 32 / kEpiParts;  // most 32-row chunks of a warp
   using Walk = TileWalk<kPair ? 2 * kTileN : kTileN, kPair ? 32 : 16>;
   extern __shared__ unsigned char smem_raw[];
   unsigned char *smem = reinterpret_cast<unsigned char *>(
@@ -414,7 +456,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       pdl_launch_dependents();
     }
     const int q = warp & 3;              // TMEM lane quadrant: channels 32 q ..
-    const int half = (warp - 2) >> 2;    // which of the quadrant's two warps
+    const int part = (warp - 2) >> 2;    // which of the quadrant's warps
     Walk walk;
     Tile t;
     uint32_t lt = 0;
@@ -423,64 +465,90 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int ch = t.ch0 + (kPair ? (int)rank * kTileN : 0) + q * 32 + lane;
       const bool valid = ch < p.n;
       const int64_t wch = (int64_t)t.g * p.n + ch;
-      const float sw = valid ? __ldg(p.sw + wch) : 0.f;
+      float sw = valid ? __ldg(p.sw + wch) : 0.f;
       const float sw2 = (kSwiGlu && valid) ? __ldg(p.sw2 + wch) : 0.f;
+      if constexpr (kOut == Out::kBlockHalf) {
+        const int eb = block_exponent(sw);
+        if (lane == 0 && valid)
+          p.exponents[(int64_t)t.g * ((p.n + 31) / 32) + ch / 32] = (uint8_t)eb;
+        sw *= __int_as_float((254 - eb) << 23) * p.unit;
+      }
+      // the rows' scales, before the wait for the tile
+      const int rows = t.row1 - t.row0;
+      float sx[kEpiChunks];
+      if constexpr (!kSplit && kOut != Out::kBlockHalf) {
+#pragma unroll
+        for (int j = 0; j < kEpiChunks; ++j) {
+          const int r = 32 * (part + j * kEpiParts) + lane;
+          sx[j] = r < rows ? p.sx[t.row0 + r] : 0.f;
+        }
+      }
       if (!mbar_wait(&tfull[acc], use & 1u, p.err)) break;
       tc_fence_after();
       const uint32_t taddr = tmem_base + ((uint32_t)(q * 32) << 16) + acc * acc_cols;
-      for (int c0 = 32 * half; c0 < t.row1 - t.row0; c0 += 64) {
+      // the accumulator is free once it is in registers
+      auto release = [&] {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          if (kPair)
+            arrive_at(at_rank(&tempty[acc], 0));
+          else
+            mbar_arrive(&tempty[acc]);
+        }
+      };
+      if (32 * part >= rows) release();
+#pragma unroll
+      for (int j = 0; j < kEpiChunks; ++j) {
+        const int c0 = 32 * (part + j * kEpiParts);
+        if (c0 >= rows) break;
         const int row = t.row0 + c0;
-        const int nr = min(32, t.row1 - row);
+        const int nr = min(32, rows - c0);
         uint32_t v[32];
         tmem_ld_32x32b_x32(taddr + c0, v);
+        uint32_t u[kSwiGlu ? 32 : 1];
+        if constexpr (kSwiGlu) tmem_ld_32x32b_x32(taddr + acc_cols / 2 + c0, u);
+        tmem_ld_wait();
+        if (c0 + 32 * kEpiParts >= rows) release();
         if constexpr (kSplit) {
           // partial sums [row][channel] over the ring, whose loads and MMAs
           // are all complete
-          tmem_ld_wait();
-          int *part = reinterpret_cast<int *>(smem) + (size_t)c0 * kTileN + q * 32 + lane;
+          int *sums = reinterpret_cast<int *>(smem) + (size_t)c0 * kTileN + q * 32 + lane;
 #pragma unroll
           for (int i = 0; i < 32; ++i)
-            if (i < nr) part[i * kTileN] = (int)v[i];
+            if (i < nr) sums[i * kTileN] = (int)v[i];
           continue;
         }
-        const float sx = lane < nr ? p.sx[row + lane] : 0.f;
-        if constexpr (kSwiGlu) {
-          uint32_t u[32];
-          tmem_ld_32x32b_x32(taddr + acc_cols / 2 + c0, u);
-          tmem_ld_wait();
-          uint16_t *dst = static_cast<uint16_t *>(p.out) + (int64_t)row * p.n + ch;
-#pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            const float a = __shfl_sync(kFull, sx, i);
-            const float g = (float)(int)v[i] * a * sw, uu = (float)(int)u[i] * a * sw2;
-            // silu(g) u, rounded once to bf16: the element type the FFN's
+        using Elt = std::conditional_t<kOut == Out::kF32, float, uint16_t>;
+        Elt *dst = static_cast<Elt *>(p.out) + (int64_t)row * p.n + ch;
+        auto value = [&](int i) -> Elt {
+          const float x = (float)(int)v[i];
+          if constexpr (kSwiGlu) {
+            const float a = __shfl_sync(kFull, sx[j], i);
+            const float g = x * a * sw, up = (float)(int)u[i] * a * sw2;
+            // silu(g) up, rounded once to bf16: the element type the FFN's
             // activations have in this library, and what is requantised.  The
             // fast exponential and quotient are good to a few units of 2^-24.
-            if (valid && i < nr)
-              dst[(int64_t)i * p.n] = bf16_bits(__fdividef(g, 1.f + __expf(-g)) * uu);
+            return bf16_bits(__fdividef(g, 1.f + __expf(-g)) * up);
+          } else if constexpr (kOut == Out::kBlockHalf) {
+            return __half_as_ushort(__float2half_rn(x * sw));
+          } else {
+            return out_value<kOut>(x * __shfl_sync(kFull, sx[j], i) * sw);
+          }
+        };
+        if (nr == 32) {
+#pragma unroll
+          for (int i = 0; i < 32; ++i, dst += p.n) {
+            const Elt y = value(i);
+            if (valid) *dst = y;
           }
         } else {
-          tmem_ld_wait();
 #pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            const float y = (float)(int)v[i] * __shfl_sync(kFull, sx, i) * sw;
-            if (valid && i < nr) {
-              const int64_t o = (int64_t)(row + i) * p.n + ch;
-              if (kOutBf16)
-                static_cast<uint16_t *>(p.out)[o] = bf16_bits(y);
-              else
-                static_cast<float *>(p.out)[o] = y;
-            }
+          for (int i = 0; i < 32; ++i, dst += p.n) {
+            const Elt y = value(i);
+            if (valid && i < nr) *dst = y;
           }
         }
-      }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) {
-        if (kPair)
-          arrive_at(at_rank(&tempty[acc], 0));
-        else
-          mbar_arrive(&tempty[acc]);
       }
     }
   }
@@ -515,10 +583,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int j = 0; j < 4; ++j)
           if (c + j < chans) {
             const float y = (float)acc4[j] * sx * __ldg(p.sw + t.ch0 + c + j);
-            if (kOutBf16)
-              static_cast<uint16_t *>(p.out)[o + j] = bf16_bits(y);
-            else
-              static_cast<float *>(p.out)[o + j] = y;
+            using Elt = decltype(out_value<kOut>(y));
+            static_cast<Elt *>(p.out)[o + j] = out_value<kOut>(y);
           }
       }
     }
@@ -571,14 +637,15 @@ size_t ring(I8Params &p, int num_w) {
 }
 
 // cluster: CTAs per cluster; units: an upper bound on the number of tiles.
-template <bool kSwiGlu, bool kOutBf16, Span kSpan>
+template <bool kSwiGlu, Out kOut, Span kSpan>
 cudaError_t launch(const CUtensorMap &tX, const CUtensorMap &tW, const CUtensorMap &tW2,
                    I8Params p, int64_t units, int cluster, int num_sms, cudaStream_t st) {
   const size_t smem = ring(p, kSwiGlu ? 2 : 1);
   if (p.stages < 2) return cudaErrorInvalidValue;
-  auto kern = k_i8_gemm<kSwiGlu, kOutBf16, kSpan>;
+  auto kern = k_i8_gemm<kSwiGlu, kOut, kSpan>;
   const cudaError_t e = ensure_smem_limit(reinterpret_cast<const void *>(kern), smem);
   if (e != cudaSuccess) return e;
+  constexpr int kThreads = block_threads<kSwiGlu, kSpan>();
   const int most = num_sms / cluster;
   const int grid = (int)(kSpan == Span::kSplit || units < most ? units : most) * cluster;
   count_launches(1);
@@ -690,14 +757,15 @@ cudaError_t launch_i8_gemm(const I8Shape &s, const DeviceInfo &dev, const int8_t
     return cudaErrorInvalidValue;
   const int64_t units = (s.T + p.bn - 1) / p.bn * p.tiles_n;
   auto go = [&](auto out) {
-    constexpr bool kOut = decltype(out)::value;
+    constexpr Out kOut = decltype(out)::value;
     if (t.pair)
       return launch<false, kOut, Span::kPair>(mX, mW, mW, p, units, 2, dev.num_sms, st);
     if (t.split > 1)
       return launch<false, kOut, Span::kSplit>(mX, mW, mW, p, units, t.split, dev.num_sms, st);
     return launch<false, kOut, Span::kOne>(mX, mW, mW, p, units, 1, dev.num_sms, st);
   };
-  return s.out_bf16 ? go(std::true_type{}) : go(std::false_type{});
+  return s.out_bf16 ? go(std::integral_constant<Out, Out::kBF16>{})
+                    : go(std::integral_constant<Out, Out::kF32>{});
 }
 
 namespace {
@@ -713,12 +781,12 @@ Tiling grouped_tiling(const ExpertShape &s) {
   const bool pair = s.slots() >= (int64_t)s.E * kPairRows;
   return tile_rows(twice < 256 ? twice : 256, 256, pair, true);
 }
-template <bool kSwiGlu, bool kOutBf16>
+template <bool kSwiGlu, Out kOut>
 cudaError_t launch_grouped(const CUtensorMap &mX, const CUtensorMap &mW, const CUtensorMap &mW2,
                            const Tiling &t, const I8Params &p, int num_sms, cudaStream_t st) {
   const int64_t units = (int64_t)p.groups * p.tiles_n + p.rows;
-  return t.pair ? launch<kSwiGlu, kOutBf16, Span::kPair>(mX, mW, mW2, p, units, 2, num_sms, st)
-                : launch<kSwiGlu, kOutBf16, Span::kOne>(mX, mW, mW2, p, units, 1, num_sms, st);
+  return t.pair ? launch<kSwiGlu, kOut, Span::kPair>(mX, mW, mW2, p, units, 2, num_sms, st)
+                : launch<kSwiGlu, kOut, Span::kOne>(mX, mW, mW2, p, units, 1, num_sms, st);
 }
 }  // namespace
 
@@ -741,12 +809,12 @@ cudaError_t launch_i8_experts_gateup(const ExpertShape &s, const DeviceInfo &dev
       !map_i8(&mG, Wg, (uint64_t)s.d, (uint64_t)s.E * s.f, kTileN) ||
       !map_i8(&mU, Wu, (uint64_t)s.d, (uint64_t)s.E * s.f, kTileN))
     return cudaErrorInvalidValue;
-  return launch_grouped<true, true>(mX, mG, mU, t, p, dev.num_sms, st);
+  return launch_grouped<true, Out::kBF16>(mX, mG, mU, t, p, dev.num_sms, st);
 }
 
 cudaError_t launch_i8_experts_down(const ExpertShape &s, const DeviceInfo &dev,
-                                   const int32_t *offsets, const int8_t *hq, const float *sh,
-                                   const int8_t *Wd, const float *sd, float *o,
+                                   const int32_t *offsets, const int8_t *hq, const int8_t *Wd,
+                                   const float *sd, uint16_t *o, uint8_t *exponents,
                                    cudaStream_t st) {
   const Tiling t = grouped_tiling(s);
   I8Params p = params(t, s.d, s.f, 1, dev.err);
@@ -754,14 +822,15 @@ cudaError_t launch_i8_experts_down(const ExpertShape &s, const DeviceInfo &dev,
   p.offsets = offsets;
   p.groups = s.E;
   p.early = true;
-  p.sx = sh;
   p.sw = sd;
   p.out = o;
+  p.exponents = exponents;
+  p.unit = expert_out_unit(s.f);
   CUtensorMap mX, mW;
   if (!map_i8(&mX, hq, (uint64_t)s.f, (uint64_t)s.slots(), (uint32_t)p.box) ||
       !map_i8(&mW, Wd, (uint64_t)s.f, (uint64_t)s.E * s.d, kTileN))
     return cudaErrorInvalidValue;
-  return launch_grouped<false, false>(mX, mW, mW, t, p, dev.num_sms, st);
+  return launch_grouped<false, Out::kBlockHalf>(mX, mW, mW, t, p, dev.num_sms, st);
 }
 
 }  // namespace sfn
