@@ -14,6 +14,8 @@ summary, "1. Architectuur" and "3. Hardware Implicaties".
 """
 from __future__ import annotations
 
+import functools
+
 from . import _capi
 from ._capi import SfnError
 
@@ -268,34 +270,52 @@ def sparse_ffn_backward(x, A, B, Wg, Wu, Wd, dy, bank: int = 64, k: int = 16,
 SCORES = {"softmax": _capi.SFN_SCORE_SOFTMAX, "sigmoid": _capi.SFN_SCORE_SIGMOID}
 
 
+# Few-token calls take a few microseconds on the GPU, about what the checks, the
+# allocation of the outputs and the C call cost on the host: what is looked up
+# per call is kept in tables.
 _fns = {}
+_elts = {}
 
 
 def _arg(t, name, where, device, shape, dtype):
     """The pointer of a contiguous CUDA tensor on `device` of this shape and dtype."""
-    torch = _torch()
-    if not isinstance(t, torch.Tensor) or not t.is_cuda or not t.is_contiguous():
-        _dev(t, name)
+    try:
+        if (t.dtype is dtype and t.shape == shape and t.device == device and t.is_cuda
+                and t.is_contiguous()):
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _dev(t, name)
     if t.device != device:
         raise ValueError(f"{where}: {name} is on {t.device}, not on {device}")
-    if t.shape != shape or t.dtype is not dtype:
-        raise ValueError(f"{where}: {name} must be {list(shape)} of {dtype}, not "
-                         f"{list(t.shape)} of {t.dtype}")
-    return t.data_ptr()
+    raise ValueError(f"{where}: {name} must be {list(shape)} of {dtype}, not "
+                     f"{list(t.shape)} of {t.dtype}")
+
+
+def _kind(dtype):
+    elt = _elts.get(dtype)
+    if elt is None:
+        elt = _elts[dtype] = _elt(dtype)
+    return elt
+
+
+def _new(device, rows, cols, dtype):
+    """A new [rows, cols] tensor (empty_strided: 1.5 us where empty takes 2.5)."""
+    return _torch().empty_strided((rows, cols), (cols, 1), dtype=dtype, device=device)
 
 
 def _run(name, device, stream, *args):
     """One C call on `stream` (default: the device's current one), with `device` current."""
-    torch = _torch()
+    cuda = _torch()._C
     fn = _fns.get(name)
     if fn is None:
         fn = _fns[name] = getattr(_capi.lib(), name)
-    st = (torch._C._cuda_getCurrentRawStream(device.index) if stream is None
-          else stream.cuda_stream)
-    if torch.cuda.current_device() == device.index:
+    index = device.index
+    st = cuda._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
+    if cuda._cuda_getDevice() == index:
         status = fn(*args, st)
     else:
-        with torch.cuda.device(device):
+        with _torch().cuda.device(device):
             status = fn(*args, st)
     if status:
         _capi.check(status, name)
@@ -303,7 +323,9 @@ def _run(name, device, stream, *args):
 
 def _scratch(workspace, nbytes, device):
     if workspace is None:
-        workspace = _torch().empty(max(nbytes, 1), dtype=_torch().uint8, device=device)
+        nbytes = max(nbytes, 1)
+        workspace = _torch().empty_strided((nbytes,), (1,), dtype=_torch().uint8, device=device)
+        return workspace.data_ptr(), nbytes, workspace
     _dev(workspace, "workspace")
     if workspace.device != device:
         raise ValueError(f"workspace is on {workspace.device}, not on {device}")
@@ -317,11 +339,14 @@ def _score(score):
 
 
 def _matrix(t, name, where):
-    if not isinstance(t, _torch().Tensor) or not t.is_cuda or not t.is_contiguous():
-        _dev(t, name)
-    if t.dim() != 2:
-        raise ValueError(f"{where}: {name} must have two dimensions")
-    return t.shape
+    try:
+        shape = t.shape
+        if len(shape) == 2 and t.is_cuda and t.is_contiguous():
+            return shape
+    except AttributeError:
+        pass
+    _dev(t, name)
+    raise ValueError(f"{where}: {name} must have two dimensions")
 
 
 def route_experts(logits, k: int, bias=None, score: str = "softmax", groups: int = 1,
@@ -338,20 +363,24 @@ def route_experts(logits, k: int, bias=None, score: str = "softmax", groups: int
     where = "route_experts"
     T, E = _matrix(logits, "logits", where)
     dev = logits.device
-    elt, kind = _elt(logits.dtype), _score(score)
+    elt, kind, slots = _kind(logits.dtype), _score(score), max(k, 0)
     bptr = None if bias is None else _arg(bias, "bias", where, dev, (E,), torch.float32)
     if experts is None:
-        experts = torch.empty((T, max(k, 0)), dtype=torch.int32, device=dev)
+        experts = _new(dev, T, slots, torch.int32)
+        eptr = experts.data_ptr()
+    else:
+        eptr = _arg(experts, "experts", where, dev, (T, slots), torch.int32)
     if weights is None:
-        weights = torch.empty((T, max(k, 0)), dtype=torch.float32, device=dev)
+        weights = _new(dev, T, slots, torch.float32)
+        wptr = weights.data_ptr()
+    else:
+        wptr = _arg(weights, "weights", where, dev, (T, slots), torch.float32)
     if scores is None and want_scores:
-        scores = torch.empty((T, E), dtype=torch.float32, device=dev)
-    eptr = _arg(experts, "experts", where, dev, (T, max(k, 0)), torch.int32)
-    wptr = _arg(weights, "weights", where, dev, (T, max(k, 0)), torch.float32)
+        scores = _new(dev, T, E, torch.float32)
     sptr = None if scores is None else _arg(scores, "scores", where, dev, (T, E),
                                             torch.float32)
     _run("sfn_route_experts", dev, stream, logits.data_ptr(), elt, bptr, eptr, wptr, sptr, T, E,
-         k, kind, groups, top_groups, group_top, int(bool(renormalize)), float(scale))
+         k, kind, groups, top_groups, group_top, 1 if renormalize else 0, scale)
     return experts, weights, scores
 
 
@@ -364,17 +393,19 @@ def route_experts_backward(logits, experts, dweights, dscores=None, score: str =
     where = "route_experts_backward"
     T, E = _matrix(logits, "logits", where)
     dev = logits.device
-    elt, kind = _elt(logits.dtype), _score(score)
-    _, k = _matrix(experts, "experts", where)
+    elt, kind = _kind(logits.dtype), _score(score)
+    k = _matrix(experts, "experts", where)[1]
     eptr = _arg(experts, "experts", where, dev, (T, k), torch.int32)
     wptr = _arg(dweights, "dweights", where, dev, (T, k), torch.float32)
     sptr = None if dscores is None else _arg(dscores, "dscores", where, dev, (T, E),
                                              torch.float32)
     if dlogits is None:
         dlogits = torch.empty_like(logits)
-    lptr = _arg(dlogits, "dlogits", where, dev, (T, E), logits.dtype)
+        lptr = dlogits.data_ptr()
+    else:
+        lptr = _arg(dlogits, "dlogits", where, dev, (T, E), logits.dtype)
     _run("sfn_route_experts_backward", dev, stream, logits.data_ptr(), elt, eptr, wptr, sptr,
-         lptr, T, E, k, kind, int(bool(renormalize)), float(scale))
+         lptr, T, E, k, kind, 1 if renormalize else 0, scale)
     return dlogits
 
 
@@ -409,16 +440,17 @@ def matmul_i8(xq, x_scale, wq, w_scale, out=None, out_dtype=None, stream=None):
     N = _matrix(wq, "wq", where)[0]
     dev = xq.device
     if out is None:
-        out = torch.empty((T, N), dtype=out_dtype or torch.bfloat16, device=dev)
+        out = _new(dev, T, N, out_dtype or torch.bfloat16)
     ptrs = [_arg(xq, "xq", where, dev, (T, K), torch.int8),
             _arg(x_scale, "x_scale", where, dev, (T,), torch.float32),
             _arg(wq, "wq", where, dev, (N, K), torch.int8),
             _arg(w_scale, "w_scale", where, dev, (N,), torch.float32),
             _arg(out, "out", where, dev, (T, N), out_dtype or out.dtype)]
-    _run("sfn_matmul_i8", dev, stream, *ptrs, _elt(out.dtype), T, N, K)
+    _run("sfn_matmul_i8", dev, stream, *ptrs, _kind(out.dtype), T, N, K)
     return out
 
 
+@functools.lru_cache(maxsize=4096)
 def linear_i8_workspace_bytes(T: int, K: int) -> int:
     return int(_capi.lib().sfn_linear_i8_workspace_bytes(T, K))
 
@@ -432,14 +464,16 @@ def linear_i8(x, wq, w_scale, out=None, out_dtype=None, workspace=None, stream=N
     T, K = _matrix(x, "x", where)
     N = _matrix(wq, "wq", where)[0]
     dev = x.device
-    if out is None:
-        out = torch.empty((T, N), dtype=out_dtype or x.dtype, device=dev)
     wptr = _arg(wq, "wq", where, dev, (N, K), torch.int8)
     sptr = _arg(w_scale, "w_scale", where, dev, (N,), torch.float32)
-    yptr = _arg(out, "out", where, dev, (T, N), out_dtype or out.dtype)
+    if out is None:
+        out = _new(dev, T, N, out_dtype or x.dtype)
+        yptr = out.data_ptr()
+    else:
+        yptr = _arg(out, "out", where, dev, (T, N), out_dtype or out.dtype)
     ws, nbytes, keep = _scratch(workspace, linear_i8_workspace_bytes(T, K), dev)
-    _run("sfn_linear_i8", dev, stream, x.data_ptr(), _elt(x.dtype), wptr, sptr, yptr,
-         _elt(out.dtype), T, N, K, ws, nbytes)
+    _run("sfn_linear_i8", dev, stream, x.data_ptr(), _kind(x.dtype), wptr, sptr, yptr,
+         _kind(out.dtype), T, N, K, ws, nbytes)
     _used_on(keep, workspace, stream)
     return out
 
@@ -450,6 +484,7 @@ def _used_on(scratch, given, stream):
         scratch.record_stream(stream)
 
 
+@functools.lru_cache(maxsize=4096)
 def experts_i8_workspace_bytes(T: int, E: int, k: int, d: int, f: int) -> int:
     return int(_capi.lib().sfn_experts_i8_workspace_bytes(T, E, k, d, f))
 
@@ -473,7 +508,7 @@ def experts_i8_forward(x, experts, weights, Wg, sg, Wu, su, Wd, sd, y=None, work
         raise ValueError(f"{where}: Wg must be [E, f, d]")
     E, f = Wg.shape[0], Wg.shape[1]
     if y is None:
-        y = torch.empty((T, d), dtype=torch.bfloat16, device=dev)
+        y = _new(dev, T, d, torch.bfloat16)
     i8, f32, bf16 = torch.int8, torch.float32, torch.bfloat16
     ptrs = [_arg(x, "x", where, dev, (T, d), bf16),
             _arg(experts, "experts", where, dev, (T, k), torch.int32),

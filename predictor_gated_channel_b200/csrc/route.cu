@@ -14,22 +14,26 @@
 // the ranking of l and is done on l itself.  With one, c is computed in
 // float32 and every decision the row took (between neighbours in the order,
 // at the k-th place, between groups) is checked against a bound on the error
-// of c; a row with a decision inside that bound is done again in float64.
+// of c; what is inside the bound is decided again in float64.
 //
 // One warp per row, V = E / 32 (rounded up to a built one) values a lane.
 // What bounds it is instruction issue, so the picks run on packed keys: the
-// score's order key with the expert's index in its low bits, one 32-bit word
-// that is unique in the row.  A lane sorts its V words once (a register
-// network); a pick is then one warp maximum (redux) over the lanes' heads, and
-// the lane that had it moves its list up.  The low bits cost the key some of
-// its mantissa: where two neighbours of the order agree in what is left, or
-// the last pick agrees with the best word left over, the row goes to the exact
-// routine (choose()), which compares whole keys.  bf16 logits fit beside the
+// score's order key with the value's place in its lane in the low bits, one
+// 32-bit word.  A lane sorts its V words once (a register network); a pick is
+// then one warp maximum (redux) over the lanes' heads, and the lane that had it
+// moves its list up.  The low bits cost the key some of its mantissa: the slots
+// are put in order by their whole scores afterwards, and only a row whose k-th
+// place the words cannot tell from the rest goes to the exact routine
+// (settle_row()), which compares whole keys.  bf16 logits fit beside the whole
 // index and are always exact.  Rows of exactly 32 V experts are loaded V
 // neighbours a lane (16-byte loads), and groups of a whole number of lanes
-// find their two largest scores with shuffles; others go through choose().
-//   4096 x 256, 8 groups: 16.8 us; 22.5 us with choose() alone (2557 instructions a row)
-//   32768 x 160, bf16:    22.5 us; 38.9 us with choose() alone (772 instructions a row)
+// find their two largest scores with shuffles; others go through settle_row().
+// What the rare paths cost is their latency, at the end of a launch: each
+// level (words, whole scores, float64 of the slots and the next two, float64 of
+// the row) is there so that few rows see the next.
+//   4096 x 256, 8 groups: 14.9 us; 22.5 us with whole keys alone (2557
+//   instructions a row), 20.9 us with float64 rows in place of float64 slots
+//   32768 x 160, bf16: 18.4 us (356 instructions a row); 38.9 us with whole keys
 //
 // The gradient: with n_i = s_i / sum_j s_j,
 //   ds_i = scale (dw_i - sum_j dw_j n_j) / sum_j s_j (renormalised), or
@@ -56,7 +60,7 @@ struct RouteParams {
   float *scores;
   int64_t T;
   int E, k, groups, group_size, top_groups, group_top;
-  bool sigmoid, renorm;
+  bool sigmoid, renorm, bf16;
   float scale;
   uint32_t low;  // the bits of a packed word that hold the index
 };
@@ -221,26 +225,44 @@ __device__ __noinline__ int choose(const R (&c)[V], const RouteParams &p, R *row
   return mine;
 }
 
-// The same choice on packed words: w[j] the order key of value j's score with
-// the index in the bits of p.low (complemented: of equal keys the lower index
-// is the larger word), 0 for a value that is out.  Lane i returns slot i's
-// word; `next` the best word left over.
 template <int V>
-__device__ __forceinline__ uint32_t choose_packed(uint32_t (&w)[V], int k, uint32_t &next) {
+__device__ __forceinline__ void sort_descending(uint32_t (&w)[V]) {
+  // Batcher's odd-even merge sort, for any V; all indices are constants
+#pragma unroll
+  for (int p = 1; p < V; p *= 2)
+#pragma unroll
+    for (int q = p; q >= 1; q /= 2)
+#pragma unroll
+      for (int j = q % p; j + q < V; j += 2 * q)
+#pragma unroll
+        for (int i = 0; i < q; ++i)
+          if (i + j + q < V && (i + j) / (2 * p) == (i + j + q) / (2 * p))
+            cex_desc(w[i + j], w[i + j + q]);
+}
+// The same choice on packed words, unique in a lane, 0 for a value that is
+// out.  Lane i returns slot i's word and, in `winner`, the lane that had it
+// (of equal words the lowest); `next` is the best word left over.
+// kUnique: no two lanes have the same word.  w: sorted, and what is left of it
+// afterwards; slots [k0, k) are filled.
+template <int V, bool kUnique>
+__device__ __forceinline__ void pick_packed(uint32_t (&w)[V], int k0, int k, uint32_t &mine,
+                                            int &winner) {
   const int lane = threadIdx.x & 31;
-  BitonicSort<0, V, 2>::run(w);
-  uint32_t mine = 0u;
-  for (int i = 0; i < k; ++i) {
+  for (int i = k0; i < k; ++i) {
     const uint32_t top = __reduce_max_sync(kFull, w[0]);
+    bool won = w[0] == top;
+    if constexpr (!kUnique) {
+      const int at = __ffs(__ballot_sync(kFull, won)) - 1;
+      won = lane == at;
+      if (lane == i) winner = at;
+    }
     if (lane == i) mine = top;
-    if (w[0] == top) {
+    if (won) {
 #pragma unroll
       for (int j = 0; j + 1 < V; ++j) w[j] = w[j + 1];
       w[V - 1] = 0u;
     }
   }
-  next = __reduce_max_sync(kFull, w[0]);
-  return mine;
 }
 
 // Bounds on the error of the float32 scores that the choice is made on
@@ -263,10 +285,18 @@ __device__ __forceinline__ float score_fast(float l, bool sigmoid, float m, floa
 }
 
 // This lane's V logits of row t (-inf past E).
+// A lane's part of a blocked row is a vector load.
+template <int V>
+constexpr bool vector_part() {
+  return (V & (V - 1)) == 0;
+}
 template <bool kBf16, int V, bool kBlocked>
 __device__ __forceinline__ void load_row(const void *logits, int64_t t, int E, float (&l)[V]) {
   const int lane = threadIdx.x & 31;
-  if constexpr (kBlocked) {
+  if constexpr (kBlocked && !vector_part<V>()) {
+#pragma unroll
+    for (int j = 0; j < V; ++j) l[j] = load_logit<kBf16>(logits, t * E + lane * V + j);
+  } else if constexpr (kBlocked) {
     constexpr int kBytes = V * (kBf16 ? 2 : 4);
     uint32_t raw[kBytes / 4];
     const char *src = static_cast<const char *>(logits) + (t * 32 + lane) * kBytes;
@@ -319,19 +349,196 @@ __device__ __forceinline__ float row_sum(const float (&l)[V], float m) {
   return z;
 }
 
+// Blocks of kWarps rows an SM holds at once (the launch bound and the grid).
+template <int V>
+constexpr int route_blocks() {
+  return V <= 4 ? 8 : (V <= 8 ? 6 : (V <= 16 ? 4 : 2));
+}
+
+// Order key of a number (not NaN): as order_key(), in three instructions.
+__device__ __forceinline__ uint32_t number_key(float f) {
+  const int b = __float_as_int(f + 0.f);  // -0 -> +0
+  return (uint32_t)(b ^ ((b >> 31) | (int)0x80000000));
+}
+
+// The choice of one row with whole keys, for rows that the packed words leave
+// undecided and for groups that are no whole number of lanes: in float32 with
+// every decision checked, and in float64 where one is inside the error bound.
+// Lane i returns slot i's expert.
+// Built once for both types and layouts and for powers of two: it is rare.
+template <int V, bool kByLogit>
+__device__ __noinline__ int settle_row(const RouteParams &p, int64_t t, double *row64) {
+  const int lane = threadIdx.x & 31;
+  float *row32 = reinterpret_cast<float *>(row64);
+  float l[V];
+  if (p.bf16)
+    load_row<true, V, false>(p.logits, t, p.E, l);
+  else
+    load_row<false, V, false>(p.logits, t, p.E, l);
+  auto logit = [&](int e) {
+    return p.bf16 ? load_logit<true>(p.logits, t * p.E + e)
+                  : load_logit<false>(p.logits, t * p.E + e);
+  };
+  int next;
+  float lo, hi;
+  if constexpr (kByLogit) {
+    return choose<V, false, float>(l, p, row32, next, lo, hi);
+  } else {
+    float bias[V];
+    bool nan = false;
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      const int e = expert_of<V, false>(j);
+      bias[j] = (p.bias != nullptr && e < p.E) ? __ldg(p.bias + e) : 0.f;
+      nan |= l[j] != l[j];
+    }
+    nan = __any_sync(kFull, nan);
+    float m = 0.f, z = 1.f;
+    if (!p.sigmoid) {
+      m = row_max<V>(l);
+      z = row_sum<V, true>(l, m);
+    }
+    if (!nan) {
+      float c[V];
+#pragma unroll
+      for (int j = 0; j < V; ++j)
+        c[j] = select_score(score_fast(l[j], p.sigmoid, m, z), l[j], bias[j]);
+      const int pick = choose<V, false, float>(c, p, row32, next, lo, hi);
+      // Is every decision outside the error of c?  Lane i < k compares slot i
+      // with slot i + 1, the last slot with the best left over.
+      auto score_at = [&](int e, float &le, float &be, float &se, float &ce) {
+        le = -INFINITY;
+        be = 0.f;
+        se = 0.f;
+        ce = -INFINITY;
+        if (e >= 0 && e < p.E) {
+          le = logit(e);
+          if (p.bias != nullptr) be = __ldg(p.bias + e);
+          se = score_fast(le, p.sigmoid, m, z);
+          ce = select_score(se, le, be);
+        }
+      };
+      float l0, b0, s0, c0, l1, b1, s1, c1;
+      score_at(pick, l0, b0, s0, c0);
+      l1 = __shfl_down_sync(kFull, l0, 1);
+      b1 = __shfl_down_sync(kFull, b0, 1);
+      s1 = __shfl_down_sync(kFull, s0, 1);
+      c1 = __shfl_down_sync(kFull, c0, 1);
+      if (lane == p.k - 1) score_at(next, l1, b1, s1, c1);
+      // equal logits with equal biases are in the right order already
+      const bool tie = l0 == l1 && b0 == b1;
+      bool unsure = lane < p.k && c0 > -INFINITY && c1 > -INFINITY && !tie &&
+                    c0 - c1 <= score_error(s0, c0, p.sigmoid) + score_error(s1, c1, p.sigmoid);
+      // at the end of the order a third value could hide behind a tie
+      if (lane == p.k - 1 && tie && c1 > -INFINITY) unsure = true;
+      if (lo > -INFINITY && hi > -INFINITY && lo < INFINITY) {
+        // a group's score sums at most two, each at most the largest score
+        const float s = p.sigmoid ? 1.f : (z > 0.f ? __fdividef(1.f, z) : 0.f);
+        unsure |= lo - hi <= 2.f * (score_error(s, lo, p.sigmoid) + score_error(s, hi, p.sigmoid)) +
+                                 4.f * kUlp * (fabsf(lo) + fabsf(hi));
+      }
+      if (!__any_sync(kFull, unsure)) return pick;
+    }
+    double z64 = 1.0, lo64, hi64;
+    if (!p.sigmoid) {
+      z64 = 0.0;
+      if (m != -INFINITY) {
+#pragma unroll 1
+        for (int j = 0; j < V; ++j) {
+          const int e = expert_of<V, false>(j);
+          if (e < p.E) z64 += exp((double)logit(e) - (double)m);
+        }
+        z64 = warp_add(z64);
+      }
+    }
+    double c64[V];
+#pragma unroll
+    for (int j = 0; j < V; ++j)
+      c64[j] = select_score(score_of<double>(l[j], p.sigmoid, m, z64), l[j], bias[j]);
+    return choose<V, false, double>(c64, p, row64, next, lo64, hi64);
+  }
+}
+
+// The row's sum of exponentials in float64; rare.
+template <bool kBf16>
+__device__ __noinline__ double row_sum64(const void *logits, int64_t t, int E, float m) {
+  double z = 0.0;
+  if (m != -INFINITY)
+    for (int e = threadIdx.x & 31; e < E; e += 32)
+      z += exp((double)load_logit<kBf16>(logits, t * E + e) - (double)m);
+  return warp_add(z);
+}
+// Does this lane's group stay?  In float64 (by logit: on the logits, exactly),
+// for groups of `per` lanes with V neighbouring experts each; rare.
+template <int V, bool kByLogit>
+__device__ __noinline__ bool settle_groups(const RouteParams &p, int64_t t, float m, int per) {
+  const int lane = threadIdx.x & 31;
+  const double z = p.sigmoid || kByLogit ? 1.0
+                   : p.bf16              ? row_sum64<true>(p.logits, t, p.E, m)
+                                         : row_sum64<false>(p.logits, t, p.E, m);
+  const double none = -INFINITY;
+  double a = none, b = none;
+  for (int j = 0; j < V; ++j) {
+    const int e = lane * V + j;
+    const float l = p.bf16 ? load_logit<true>(p.logits, t * p.E + e)
+                           : load_logit<false>(p.logits, t * p.E + e);
+    const float be = p.bias != nullptr ? __ldg(p.bias + e) : 0.f;
+    const double c =
+        kByLogit ? (double)l : select_score(score_of<double>(l, p.sigmoid, m, z), l, be);
+    b = fmax(b, fmin(a, c));
+    a = fmax(a, c);
+  }
+  for (int o = per >> 1; o > 0; o >>= 1) {
+    const double a2 = __shfl_xor_sync(kFull, a, o), b2 = __shfl_xor_sync(kFull, b, o);
+    b = fmax(fmax(b, b2), fmin(a, a2));
+    a = fmax(a, a2);
+  }
+  const double gs = (p.group_top == 2 && b != none) ? a + b : a;
+  int rank = 0;
+  for (int h = 0; h < p.groups; ++h) {
+    const double hs = __shfl_sync(kFull, gs, h * per);
+    rank += (hs > gs) | ((hs == gs) & (h < lane / per));
+  }
+  return rank < p.top_groups;
+}
+
+// Does (score c1, expert e1) come before (c0, e0)?  Those at -inf are empty
+// slots in any order.
+template <class R>
+__device__ __forceinline__ bool before(R c1, int e1, R c0, int e0) {
+  return c0 < c1 || (c0 == c1 && e0 > e1 && c0 > (R)-INFINITY);
+}
+// Lanes [0, n) in order, by exchanges of neighbours; rare.
+template <class R>
+__device__ __noinline__ void exchange_sort(int n, R &c, int &e, float &l, float &b) {
+  const int lane = threadIdx.x & 31;
+  for (int i = 0; i < n; ++i) {
+    const int other = (i & 1) ? ((lane - 1) ^ 1) + 1 : lane ^ 1;
+    const bool both = other >= 0 && other < n && lane < n;
+    const int from = both ? other : lane;
+    const R c2 = __shfl_sync(kFull, c, from);
+    const int e2 = __shfl_sync(kFull, e, from);
+    const float l2 = __shfl_sync(kFull, l, from), b2 = __shfl_sync(kFull, b, from);
+    if (both && (lane < other ? before(c2, e2, c, e) : before(c, e, c2, e2))) {
+      c = c2;
+      e = e2;
+      l = l2;
+      b = b2;
+    }
+  }
+}
 // kByLogit: no bias, and groups (if any) scored by their largest: the logits
 // themselves are ranked.  kGroups: groups > 1.
 template <bool kBf16, int V, bool kBlocked, bool kByLogit, bool kGroups>
-__global__ void __launch_bounds__(32 * kWarps) k_route(const RouteParams p) {
+__global__ void __launch_bounds__(32 * kWarps, route_blocks<V>()) k_route(const RouteParams p) {
   extern __shared__ double route_smem[];
   pdl_wait();
   pdl_launch_dependents();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  double *row64 = route_smem + (size_t)warp * (kGroups ? p.E : 0);
-  float *row32 = reinterpret_cast<float *>(row64);
   // groups of a whole number of lanes; then every lane of a group knows it
-  const bool lanes_per_group = kGroups && kBlocked && 32 % p.groups == 0;
+  const bool packed = !kGroups || (kBlocked && 32 % p.groups == 0);
   const int per = kGroups ? 32 / p.groups : 32;
+  const uint32_t none = order_key(-INFINITY);
   float bias[kByLogit ? 1 : V];
   if constexpr (!kByLogit) {
 #pragma unroll
@@ -340,10 +547,21 @@ __global__ void __launch_bounds__(32 * kWarps) k_route(const RouteParams p) {
       bias[j] = (p.bias != nullptr && e < p.E) ? __ldg(p.bias + e) : 0.f;
     }
   }
+  // packed words: the order key with this value's place in its lane below it
+  // (complemented: of equal keys the lower index is the larger word); for bf16
+  // logits the whole index, which fits below their 16 bits
+  constexpr bool kWhole = kByLogit && kBf16;
+  constexpr uint32_t kPlaces = V <= 1 ? 0u : V <= 2 ? 1u : V <= 4 ? 3u : V <= 8 ? 7u : V <= 16 ? 15u : 31u;
+  const uint32_t low = kWhole ? p.low : kPlaces;
   const int64_t stride = (int64_t)gridDim.x * kWarps;
-  for (int64_t t = (int64_t)blockIdx.x * kWarps + warp; t < p.T; t += stride) {
+  int64_t t = (int64_t)blockIdx.x * kWarps + warp;
+  float ahead[V];  // the next row's logits, on their way while this one is done
+  if (t < p.T) load_row<kBf16, V, kBlocked>(p.logits, t, p.E, ahead);
+  for (; t < p.T; t += stride) {
     float l[V];
-    load_row<kBf16, V, kBlocked>(p.logits, t, p.E, l);
+#pragma unroll
+    for (int j = 0; j < V; ++j) l[j] = ahead[j];
+    if (t + stride < p.T) load_row<kBf16, V, kBlocked>(p.logits, t + stride, p.E, ahead);
     bool nan = false;
 #pragma unroll
     for (int j = 0; j < V; ++j) nan |= l[j] != l[j];
@@ -363,18 +581,26 @@ __global__ void __launch_bounds__(32 * kWarps) k_route(const RouteParams p) {
         if (expert_of<V, kBlocked>(j) < p.E)
           p.scores[t * p.E + expert_of<V, kBlocked>(j)] = score_of<float>(l[j], p.sigmoid, m, z);
     }
-    float c[V];
+    const bool slot = lane < p.k;  // lane i < k has slot i
+    int pick = -1;
+    float lp = -INFINITY, bp = 0.f;  // its logit and bias
+    auto look_up = [&] {
+      lp = -INFINITY;
+      bp = 0.f;
+      if (slot && pick >= 0 && pick < p.E) {
+        lp = load_logit<kBf16>(p.logits, t * p.E + pick);
+        if (!kByLogit && p.bias != nullptr) bp = __ldg(p.bias + pick);
+      }
+    };
+    bool unsure = nan || !packed;
+    if (!unsure) {
+      float c[V];
 #pragma unroll
-    for (int j = 0; j < V; ++j)
-      c[j] = kByLogit ? l[j]
-                      : select_score(score_fast(l[j], p.sigmoid, m, z_fast), l[j], bias[j]);
-
-    int pick = -1, next = kNone;
-    float lo = INFINITY, hi = -INFINITY;  // as in choose()
-    float rest = -INFINITY;               // no score left over is above this
-    bool unsure = nan;
-    const bool packed = !nan && (!kGroups || lanes_per_group);
-    if (packed) {
+      for (int j = 0; j < V; ++j)
+        c[j] = kByLogit ? l[j]
+                        : select_score(score_fast(l[j], p.sigmoid, m, z_fast), l[j], bias[j]);
+      // the largest score there can be, for the error bounds
+      const float most = p.sigmoid || kByLogit ? 1.f : (z_fast > 0.f ? __fdividef(1.f, z_fast) : 0.f);
       bool in = true;  // this lane's group stays
       if (kGroups) {
         float a = -INFINITY, b = -INFINITY;
@@ -389,135 +615,121 @@ __global__ void __launch_bounds__(32 * kWarps) k_route(const RouteParams p) {
           a = fmaxf(a, a2);
         }
         const float gs = (p.group_top == 2 && b != -INFINITY) ? a + b : a;
-        uint32_t word = (order_key(gs) & ~31u) | (uint32_t)(31 - lane / per);
+        uint32_t word = (number_key(gs) & ~31u) | (uint32_t)(31 - lane / per);
         uint32_t last = 0u;
         in = false;
         for (int i = 0; i < p.top_groups; ++i) {
           last = __reduce_max_sync(kFull, word);
           if (word == last) {
             in = true;
-            lo = gs;
             word = 0u;
           }
         }
         const uint32_t left = __reduce_max_sync(kFull, word);
-        if (left != 0u) {
-          // the worst kept group and the most a dropped one can have; equal in
-          // what the packed word keeps: undecided
-          const uint32_t none = order_key(-INFINITY) & ~31u;
-          unsure |= (left & ~31u) == (last & ~31u) && (last & ~31u) != none;
-          hi = (left & ~31u) == none ? -INFINITY : key_value(left | 31u);
-          const uint32_t lk = __reduce_min_sync(kFull, in ? order_key(gs) : 0xffffffffu);
-          lo = key_value(lk);
+        if (left != 0u && (last & ~31u) != (none & ~31u) && (left & ~31u) != (none & ~31u)) {
+          // may the worst kept group and the best dropped one have changed
+          // places?  First by the words (32 units of the last place apart),
+          // then by the whole scores.  A group's score sums at most two.
+          auto close = [&](float lo, float hi) {
+            return kByLogit ? lo <= hi
+                            : lo - hi <= 2.f * (score_error(most, lo, p.sigmoid) +
+                                                score_error(most, hi, p.sigmoid)) +
+                                             4.f * kUlp * (fabsf(lo) + fabsf(hi));
+          };
+          if (close(key_value(last & ~31u), key_value(left | 31u))) {
+            const uint32_t key = number_key(gs);
+            const float lo = key_value(__reduce_min_sync(kFull, in ? key : 0xffffffffu));
+            const float hi = key_value(__reduce_max_sync(kFull, in ? 0u : key));
+            if (close(lo, hi)) in = settle_groups<V, kByLogit>(p, t, m, per);
+          }
         }
       }
       uint32_t w[V];
 #pragma unroll
       for (int j = 0; j < V; ++j) {
         const uint32_t e = (uint32_t)expert_of<V, kBlocked>(j);
-        w[j] = (in && (kBlocked || e < (uint32_t)p.E))
-                   ? (order_key(c[j]) & ~p.low) | (p.low - e) : 0u;
+        const uint32_t place = kWhole ? p.low - e : kPlaces - (uint32_t)j;
+        w[j] = (in && (kBlocked || e < (uint32_t)p.E)) ? (number_key(c[j]) & ~low) | place : 0u;
       }
-      uint32_t left;
-      const uint32_t mine = choose_packed<V>(w, p.k, left);
-      pick = lane < p.k ? (int)(p.low - (mine & p.low)) : -1;
-      uint32_t after = __shfl_down_sync(kFull, mine, 1);
-      if (lane == p.k - 1) after = left;
-      // do neighbours differ in what the words keep?  Those at -inf are all
-      // empty slots, whichever they are.
-      if (!(kByLogit && kBf16) && lane < p.k && (mine & ~p.low) == (after & ~p.low) &&
-          after != 0u && (mine & ~p.low) != (order_key(-INFINITY) & ~p.low)) {
-        // inside the order: equal logits with equal biases are in the right
-        // order already; at its end a third value could hide
-        bool tie = false;
-        if (lane < p.k - 1) {
-          const int ea = (int)(p.low - (after & p.low));
-          tie = load_logit<kBf16>(p.logits, t * p.E + pick) ==
-                load_logit<kBf16>(p.logits, t * p.E + ea);
-          if (!kByLogit && p.bias != nullptr)
-            tie = tie && __ldg(p.bias + pick) == __ldg(p.bias + ea);
+      uint32_t mine = 0u;
+      int winner = 0;
+      sort_descending<V>(w);
+      pick_packed<V, kWhole>(w, 0, p.k, mine, winner);
+      if constexpr (kWhole) {
+        if (slot) {
+          pick = (int)(p.low - (mine & p.low));
+          const uint32_t kept = mine & ~low;
+          // a bf16's key is all in the upper half (negative numbers: complemented)
+          lp = __uint_as_float((kept & 0x80000000u) ? kept & 0x7fff0000u : ~kept & 0xffff0000u);
         }
-        unsure |= !tie;
-      }
-      if (left != 0u) {
-        next = (int)(p.low - (left & p.low));
-        rest = key_value(left | p.low);
-      }
-    } else if (!nan) {
-      pick = choose<V, kBlocked, float>(c, p, row32, next, lo, hi);
-    }
-    if (!kByLogit && !nan) {
-      // Is every decision outside the error of c?  Lane i < k compares slot i
-      // with slot i + 1, the last slot with what is left over.
-      auto score_at = [&](int e, float &le, float &be, float &se, float &ce) {
-        le = -INFINITY;
-        be = 0.f;
-        se = 0.f;
-        ce = -INFINITY;
-        if (e >= 0 && e < p.E) {
-          le = load_logit<kBf16>(p.logits, t * p.E + e);
-          if (p.bias != nullptr) be = __ldg(p.bias + e);
-          se = score_fast(le, p.sigmoid, m, z_fast);
-          ce = select_score(se, le, be);
+      } else {
+        auto expert_at = [&] {
+          const int place = (int)(kPlaces - (mine & kPlaces));
+          return kBlocked ? winner * V + place : winner + 32 * place;
+        };
+        if (slot) pick = expert_at();
+        look_up();
+        float cp = -INFINITY;  // the slot's selection score in full
+        if (slot)
+          cp = kByLogit ? lp : select_score(score_fast(lp, p.sigmoid, m, z_fast), lp, bp);
+        // neighbours whose words agree may be in the wrong order: exchange
+        // them, by whole scores and then by index
+        float c1 = __shfl_down_sync(kFull, cp, 1);
+        const int e1 = __shfl_down_sync(kFull, pick, 1);
+        if (__any_sync(kFull, lane < p.k - 1 && before(c1, e1, cp, pick))) {
+          exchange_sort(p.k, cp, pick, lp, bp);
+          c1 = __shfl_down_sync(kFull, cp, 1);
         }
-      };
-      float l0, b0, s0, c0, l1, b1, s1, c1;
-      score_at(pick, l0, b0, s0, c0);
-      l1 = __shfl_down_sync(kFull, l0, 1);
-      b1 = __shfl_down_sync(kFull, b0, 1);
-      s1 = __shfl_down_sync(kFull, s0, 1);
-      c1 = __shfl_down_sync(kFull, c0, 1);
-      bool tie = l0 == l1 && b0 == b1;
-      if (lane == p.k - 1) {
-        score_at(next, l1, b1, s1, c1);
-        // every score left over is within the packed word's resolution of this
-        // one: the bound on the largest, with the largest possible s
-        tie = !packed && l0 == l1 && b0 == b1;
-        if (packed) {
-          c1 = rest;
-          s1 = p.sigmoid ? 1.f : (z_fast > 0.f ? __fdividef(1.f, z_fast) : 0.f);
+        // the most that what is left over can have, against the last slot
+        uint32_t left = __reduce_max_sync(kFull, w[0]);
+        bool rest = left != 0u && (left & ~low) != (none & ~low);
+        if constexpr (kByLogit) {
+          unsure |= lane == p.k - 1 && rest && cp <= key_value(left | low);
+        } else {
+          auto bound = [&](float c) { return score_error(most, c, p.sigmoid); };
+          const float l1 = __shfl_down_sync(kFull, lp, 1), b1 = __shfl_down_sync(kFull, bp, 1);
+          bool close = false;
+          if (slot && cp > -INFINITY) {
+            if (lane == p.k - 1) {
+              const float hi = key_value(left | low);
+              close = rest && cp - hi <= bound(cp) + bound(hi);
+            } else {  // equal logits with equal biases are in the right order
+              close = c1 > -INFINITY && !(lp == l1 && bp == b1) &&
+                      cp - c1 <= bound(cp) + bound(c1);
+            }
+          }
+          if (!__any_sync(kFull, unsure) && __any_sync(kFull, close)) {
+            // inside the error of float32: the slots and the next two, in
+            // float64, and the order again; undecided only if what is left
+            // over is that close too
+            const int kx = min(p.k + 2, 32);
+            pick_packed<V, false>(w, p.k, kx, mine, winner);
+            left = __reduce_max_sync(kFull, w[0]);
+            rest = left != 0u && (left & ~low) != (none & ~low);
+            const bool more = lane >= p.k && lane < kx && mine != 0u;
+            if (more) {
+              pick = expert_at();
+              lp = load_logit<kBf16>(p.logits, t * p.E + pick);
+              if (p.bias != nullptr) bp = __ldg(p.bias + pick);
+            }
+            const double z64 = p.sigmoid ? 1.0 : row_sum64<kBf16>(p.logits, t, p.E, m);
+            double c64 = -INFINITY;
+            if (slot || more)
+              c64 = select_score(score_of<double>(lp, p.sigmoid, m, z64), lp, bp);
+            exchange_sort(kx, c64, pick, lp, bp);
+            const double last = __shfl_sync(kFull, c64, p.k - 1);
+            const float hi = key_value(left | low);
+            unsure = rest && (float)last - hi <= bound(hi) + 2.f * kUlp * fabsf(hi);
+          }
         }
-      }
-      if (lane < p.k && c0 > -INFINITY && c1 > -INFINITY && !tie)
-        unsure |= c0 - c1 <= score_error(s0, c0, p.sigmoid) + score_error(s1, c1, p.sigmoid);
-      if (kGroups && lo > -INFINITY && hi > -INFINITY && lo < INFINITY) {
-        // a group's score sums at most two, each at most the largest score
-        const float s = p.sigmoid ? 1.f : (z_fast > 0.f ? __fdividef(1.f, z_fast) : 0.f);
-        unsure |= lo - hi <= 2.f * (score_error(s, lo, p.sigmoid) + score_error(s, hi, p.sigmoid)) +
-                                 4.f * kUlp * (fabsf(lo) + fabsf(hi));
       }
     }
     if (__any_sync(kFull, unsure)) {
-      if constexpr (kByLogit) {
-        pick = choose<V, kBlocked, float>(c, p, row32, next, lo, hi);
-      } else {
-        double z64 = 1.0, lo64, hi64;
-        if (!p.sigmoid) {
-          z64 = 0.0;
-          if (m != -INFINITY) {
-#pragma unroll 1
-            for (int j = 0; j < V; ++j) {
-              const int e = expert_of<V, kBlocked>(j);
-              if (e < p.E)
-                z64 += exp((double)load_logit<kBf16>(p.logits, t * p.E + e) - (double)m);
-            }
-            z64 = warp_add(z64);
-          }
-        }
-        double c64[V];
-#pragma unroll
-        for (int j = 0; j < V; ++j)
-          c64[j] = select_score(score_of<double>(l[j], p.sigmoid, m, z64), l[j], bias[j]);
-        pick = choose<V, kBlocked, double>(c64, p, row64, next, lo64, hi64);
-      }
+      constexpr int kPow2 = (int)kPlaces + 1;
+      pick = settle_row<kPow2, kByLogit>(p, t, route_smem + (size_t)warp * (kGroups ? p.E : 0));
+      look_up();
     }
-    // weights: lane i < k has slot i
-    const bool slot = lane < p.k;
-    float lp = -INFINITY;
-    if (slot && pick >= 0 && pick < p.E) {
-      lp = load_logit<kBf16>(p.logits, t * p.E + pick);
-      if (!kByLogit && p.bias != nullptr && __ldg(p.bias + pick) == -INFINITY) lp = -INFINITY;
-    }
+    if (bp == -INFINITY) lp = -INFINITY;
     const bool empty = lp == -INFINITY;
     float w;
     if (p.renorm && !p.sigmoid) {
@@ -560,6 +772,12 @@ __device__ __forceinline__ void store_grad(void *p, int64_t i, float g) {
     static_cast<float *>(p)[i] = g;
 }
 
+__device__ __forceinline__ uint32_t pack_bf16x2(float lower, float upper) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(upper), "f"(lower));
+  return r;
+}
+
 // This lane's V gradients of row t.
 template <bool kBf16, int V, bool kBlocked>
 __device__ __forceinline__ void store_row(void *out, int64_t t, int E, const float (&g)[V]) {
@@ -569,8 +787,7 @@ __device__ __forceinline__ void store_row(void *out, int64_t t, int E, const flo
     uint32_t raw[kBytes / 4];
 #pragma unroll
     for (int i = 0; i < kBytes / 4; ++i)
-      raw[i] = kBf16 ? (uint32_t)f32_to_bf16_bits(g[kBf16 ? 2 * i : i]) |
-                           ((uint32_t)f32_to_bf16_bits(g[kBf16 ? 2 * i + 1 : i]) << 16)
+      raw[i] = kBf16 ? pack_bf16x2(g[kBf16 ? 2 * i : i], g[kBf16 ? 2 * i + 1 : i])
                      : __float_as_uint(g[kBf16 ? 0 : i]);
     char *dst = static_cast<char *>(out) + (t * 32 + lane) * kBytes;
     if constexpr (kBytes >= 16) {
@@ -590,44 +807,72 @@ __device__ __forceinline__ void store_row(void *out, int64_t t, int E, const flo
   }
 }
 
-// One warp per row: the row's dense part (zero without one) in whole rows,
-// then, after a warp barrier that orders the two, the chosen experts' full
-// gradients over it, lane i slot i's.
+// Blocks of kWarps rows an SM holds at once.
+template <int V>
+constexpr int backward_blocks() {
+  return V <= 4 ? 10 : (V <= 8 ? 6 : (V <= 16 ? 4 : 2));
+}
+
+// One warp per row.
 // kDense: every score of the row is needed (softmax without renormalisation,
-// or a dscores).  Otherwise the gradient outside the chosen experts is 0: for
-// the renormalised softmax sum_e s_e ds_e = scale (sum_i dw_i n_i -
-// sum_j dw_j n_j sum_i n_i) / D = 0, and s_i / D needs the chosen logits only.
+// or a dscores): the slots' ds are added to the lanes' values in slot order,
+// and the row is written once.  Otherwise the gradient outside the chosen
+// experts is 0: for the renormalised softmax sum_e s_e ds_e = scale (sum_i dw_i
+// n_i - sum_j dw_j n_j sum_i n_i) / D = 0, and s_i / D needs the chosen logits
+// only; the row is written as zeros and, after a warp barrier that orders the
+// two, the chosen experts' gradients over it, lane i slot i's.
 template <bool kBf16, int V, bool kBlocked, bool kDense>
-__global__ void __launch_bounds__(32 * kWarps) k_route_bwd(const RouteBwdParams p) {
+__global__ void __launch_bounds__(32 * kWarps, backward_blocks<V>())
+    k_route_bwd(const RouteBwdParams p) {
   pdl_wait();
   pdl_launch_dependents();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t stride = (int64_t)gridDim.x * kWarps;
-  for (int64_t t = (int64_t)blockIdx.x * kWarps + warp; t < p.T; t += stride) {
-    // lane i < k: slot i
-    int e = -1;
-    float le = -INFINITY, dw = 0.f;
+  // the next row's inputs are on their way while this one is done
+  constexpr int kRow = kDense ? V : 1;
+  int next_e = -1;
+  float next_dw = 0.f, next_l[kRow], next_ds[kRow];
+  auto fetch = [&](int64_t t) {
     if (lane < p.k) {
-      e = p.experts[t * p.k + lane];
-      dw = p.dweights[t * p.k + lane];
-      if (e < 0 || e >= p.E) e = -1;
+      next_e = p.experts[t * p.k + lane];
+      next_dw = p.dweights[t * p.k + lane];
     }
-    float l[kDense ? V : 1], ds[kDense ? V : 1];
     if constexpr (kDense) {
-      load_row<kBf16, V, kBlocked>(p.logits, t, p.E, l);
-      if (p.dscores != nullptr)
-        load_row<false, V, kBlocked>(p.dscores, t, p.E, ds);
-      else
-#pragma unroll
-        for (int j = 0; j < V; ++j) ds[j] = 0.f;
+      load_row<kBf16, V, kBlocked>(p.logits, t, p.E, next_l);
+      if (p.dscores != nullptr) load_row<false, V, kBlocked>(p.dscores, t, p.E, next_ds);
     }
+  };
+  int64_t t = (int64_t)blockIdx.x * kWarps + warp;
+  if (t < p.T) fetch(t);
+  for (; t < p.T; t += stride) {
+    // lane i < k: slot i
+    const int e = next_e >= 0 && next_e < p.E ? next_e : -1;
+    const float dw = next_dw;
+    float le = -INFINITY, l[kRow], ds[kRow];
     if (e >= 0) le = load_logit<kBf16>(p.logits, t * p.E + e);
-    const bool dense = kDense;
+    if constexpr (kDense) {
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        l[j] = next_l[j];
+        ds[j] = p.dscores != nullptr ? next_ds[j] : 0.f;
+      }
+    }
+    if (t + stride < p.T) fetch(t + stride);
     float m = 0.f, z = 1.f;
     if (!p.sigmoid) {
       if constexpr (kDense) {
+        // l becomes the row's scores
         m = row_max<V>(l);
-        z = row_sum<V, false>(l, m);
+        z = 0.f;
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+          l[j] = m == -INFINITY ? 0.f : expf(l[j] - m);
+          z += l[j];
+        }
+        z = warp_add(z);
+        const float inv = z == 0.f ? 0.f : 1.f / z;
+#pragma unroll
+        for (int j = 0; j < V; ++j) l[j] *= inv;
       } else {
         // only the ratio to the chosen experts' sum matters
         const uint32_t key = __reduce_max_sync(kFull, e >= 0 ? order_key(le) : 0u);
@@ -635,34 +880,28 @@ __global__ void __launch_bounds__(32 * kWarps) k_route_bwd(const RouteBwdParams 
         if (m == -INFINITY) z = 0.f;
       }
     }
-    const float s = e >= 0 ? score_of<float>(le, p.sigmoid, m, z) : 0.f;
-    float d = p.scale * dw;
+    float d = p.scale * dw, s = 0.f;
+    if (p.renorm || !kDense) s = e >= 0 ? score_of<float>(le, p.sigmoid, m, z) : 0.f;
     if (p.renorm) {
       const float sum = warp_add(s);
       const float mean = sum == 0.f ? 0.f : warp_add(dw * s) / sum;
       d = sum == 0.f ? 0.f : p.scale * (dw - mean) / sum;
     }
-    if (e < 0) d = 0.f;
-    float dot = 0.f;
-    if (kDense && !p.sigmoid) dot = s * d;
-    // the same expert in two slots: the first of them takes the sum
-    bool first = e >= 0;
-    const uint32_t same = __match_any_sync(kFull, e >= 0 ? e : -1 - lane);
-    if (__any_sync(kFull, __popc(same) > 1)) {
-      float sum = 0.f;
-      for (int i = 0; i < p.k; ++i) {
-        const float di = __shfl_sync(kFull, d, i);
-        if ((same >> i) & 1u) sum += di;
-      }
-      d = sum;
-      first = first && __ffs(same) - 1 == lane;
-    }
     float g[V];
     if constexpr (kDense) {
+      for (int i = 0; i < p.k; ++i) {
+        const int ei = __shfl_sync(kFull, e, i);
+        const float di = __shfl_sync(kFull, d, i);
+        // the owner lane and the value's place in it (-1: an empty slot, nobody)
+        const int at = ei < 0 ? -1 : (kBlocked ? ei - lane * V : ((ei & 31) == lane ? ei >> 5 : -1));
+#pragma unroll
+        for (int j = 0; j < V; ++j)
+          if (at == j) ds[j] += di;
+      }
       if (!p.sigmoid) {
+        float dot = 0.f;
 #pragma unroll
         for (int j = 0; j < V; ++j) {
-          l[j] = score_of<float>(l[j], false, m, z);
           // values past E have the score 0; their ds must not be -inf
           if (!kBlocked && expert_of<V, kBlocked>(j) >= p.E) ds[j] = 0.f;
           dot += l[j] * ds[j];
@@ -678,46 +917,55 @@ __global__ void __launch_bounds__(32 * kWarps) k_route_bwd(const RouteBwdParams 
           g[j] = ds[j] * (x * q) * q;
         }
       }
+      store_row<kBf16, V, kBlocked>(p.dlogits, t, p.E, g);
     } else {
 #pragma unroll
       for (int j = 0; j < V; ++j) g[j] = 0.f;
-    }
-    store_row<kBf16, V, kBlocked>(p.dlogits, t, p.E, g);
-    __syncwarp();
-    if (first) {
-      const float all = d + ((dense && p.dscores != nullptr) ? __ldg(p.dscores + t * p.E + e) : 0.f);
-      float ge;
-      if (p.sigmoid) {
-        const float x = expf(-fabsf(le)), q = 1.f / (1.f + x);
-        ge = all * (x * q) * q;
-      } else {
-        ge = s * (all - dot);
+      store_row<kBf16, V, kBlocked>(p.dlogits, t, p.E, g);
+      // the same expert in two slots: the first of them takes the sum
+      if (e < 0) d = 0.f;
+      bool first = e >= 0;
+      const uint32_t same = __match_any_sync(kFull, e >= 0 ? e : -1 - lane);
+      if (__any_sync(kFull, __popc(same) > 1)) {
+        float sum = 0.f;
+        for (int i = 0; i < p.k; ++i) {
+          const float di = __shfl_sync(kFull, d, i);
+          if ((same >> i) & 1u) sum += di;
+        }
+        d = sum;
+        first = first && __ffs(same) - 1 == lane;
       }
-      store_grad<kBf16>(p.dlogits, t * p.E + e, ge);
+      __syncwarp();
+      if (first) {
+        float ge = s * d;
+        if (p.sigmoid) {
+          const float x = expf(-fabsf(le)), q = 1.f / (1.f + x);
+          ge = d * (x * q) * q;
+        }
+        store_grad<kBf16>(p.dlogits, t * p.E + e, ge);
+      }
     }
   }
 }
 
-int route_grid(int64_t T, int num_sms) {
-  const int64_t blocks = (T + kWarps - 1) / kWarps;
-  const int64_t most = (int64_t)num_sms * 16;
-  return (int)(blocks < most ? blocks : most);
-}
-
-// f(V, blocked) with the smallest built V with 32 V >= E; blocked: the rows
-// are exactly 32 V long and their 16-byte pieces aligned.
+// f(V, blocked) with the smallest built V with 32 V >= E; blocked (V
+// neighbours a lane): the rows are exactly 32 V long, and a lane's part is an
+// aligned vector load or groups need their experts side by side.
 template <class F>
-cudaError_t with_layout(int E, bool aligned, F &&f) {
+cudaError_t with_layout(int E, bool aligned, bool groups, F &&f) {
   auto with_v = [&](auto v) {
     constexpr int V = decltype(v)::value;
     if constexpr (V > 1)
-      if (E == 32 * V && aligned) return f(v, std::true_type{});
+      if (E == 32 * V && (vector_part<V>() ? aligned : groups)) return f(v, std::true_type{});
     return f(v, std::false_type{});
   };
   if (E <= 32) return with_v(std::integral_constant<int, 1>{});
   if (E <= 64) return with_v(std::integral_constant<int, 2>{});
   if (E <= 128) return with_v(std::integral_constant<int, 4>{});
+  if (E <= 160) return with_v(std::integral_constant<int, 5>{});
+  if (E <= 192) return with_v(std::integral_constant<int, 6>{});
   if (E <= 256) return with_v(std::integral_constant<int, 8>{});
+  if (E <= 384) return with_v(std::integral_constant<int, 12>{});
   if (E <= 512) return with_v(std::integral_constant<int, 16>{});
   return with_v(std::integral_constant<int, 32>{});
 }
@@ -730,10 +978,12 @@ bool aligned16(std::initializer_list<const void *> ps) {
 
 // The kernel's grid: blocks of kWarps rows, at most what the SMs hold at once.
 template <class P>
-cudaError_t launch_rows(void (*kern)(P), int64_t T, size_t smem, int num_sms, cudaStream_t st,
-                        const P &p) {
+cudaError_t launch_rows(void (*kern)(P), int64_t T, int blocks_per_sm, size_t smem, int num_sms,
+                        cudaStream_t st, const P &p) {
+  const int64_t blocks = (T + kWarps - 1) / kWarps, most = (int64_t)num_sms * blocks_per_sm;
   count_launches(1);
-  return launch_pdl(kern, dim3(route_grid(T, num_sms)), dim3(32 * kWarps), smem, st, p);
+  return launch_pdl(kern, dim3((unsigned)(blocks < most ? blocks : most)), dim3(32 * kWarps), smem,
+                    st, p);
 }
 
 }  // namespace
@@ -742,17 +992,22 @@ cudaError_t launch_route(const RouteShape &s, const void *logits, const float *b
                          int32_t *experts, float *weights, float *scores, int num_sms,
                          cudaStream_t st) {
   RouteParams p{logits, bias, experts, weights, scores, s.T, s.E, s.k, s.groups,
-                s.E / s.groups, s.top_groups, s.group_top, s.sigmoid, s.renorm, s.scale, 1u};
+                s.E / s.groups, s.top_groups, s.group_top, s.sigmoid, s.renorm, s.bf16, s.scale, 1u};
   while (p.low + 1 < (uint32_t)s.E) p.low = 2 * p.low + 1;  // index bits of a packed word
   const bool by_logit = bias == nullptr && (s.groups == 1 || s.group_top == 1);
   const bool groups = s.groups > 1;
   const size_t smem = groups ? (size_t)kWarps * s.E * sizeof(double) : 0;
-  return with_layout(s.E, aligned16({logits}), [&](auto v, auto blocked) {
+  return with_layout(s.E, aligned16({logits}), groups, [&](auto v, auto blocked) {
     constexpr int V = decltype(v)::value;
     constexpr bool kB = decltype(blocked)::value;
     auto go = [&](auto bf16, auto logit, auto grouped) {
-      return launch_rows(k_route<decltype(bf16)::value, V, kB, decltype(logit)::value,
-                                 decltype(grouped)::value>, s.T, smem, num_sms, st, p);
+      // (not reached, and not built)
+      if constexpr (kB && !vector_part<V>() && !decltype(grouped)::value)
+        return cudaErrorInvalidValue;
+      else
+        return launch_rows(k_route<decltype(bf16)::value, V, kB, decltype(logit)::value,
+                                 decltype(grouped)::value>, s.T, route_blocks<V>(), smem, num_sms, st,
+                         p);
     };
     auto with_groups = [&](auto bf16, auto logit) {
       return groups ? go(bf16, logit, std::true_type{}) : go(bf16, logit, std::false_type{});
@@ -771,12 +1026,15 @@ cudaError_t launch_route_backward(const RouteShape &s, const void *logits,
   const RouteBwdParams p{logits, experts, dweights, dscores, dlogits, s.T,
                          s.E,    s.k,     s.sigmoid, s.renorm, s.scale};
   const bool dense = dscores != nullptr || (!s.sigmoid && !s.renorm);
-  return with_layout(s.E, aligned16({logits, dscores, dlogits}), [&](auto v, auto blocked) {
+  return with_layout(s.E, aligned16({logits, dscores, dlogits}), false, [&](auto v, auto blocked) {
     constexpr int V = decltype(v)::value;
     constexpr bool kB = decltype(blocked)::value;
     auto go = [&](auto bf16, auto all) {
-      return launch_rows(k_route_bwd<decltype(bf16)::value, V, kB, decltype(all)::value>, s.T, 0,
-                         num_sms, st, p);
+      if constexpr (kB && !vector_part<V>())  // (not reached, and not built)
+        return cudaErrorInvalidValue;
+      else
+        return launch_rows(k_route_bwd<decltype(bf16)::value, V, kB, decltype(all)::value>, s.T,
+                         backward_blocks<V>(), 0, num_sms, st, p);
     };
     auto with_all = [&](auto bf16) {
       return dense ? go(bf16, std::true_type{}) : go(bf16, std::false_type{});
