@@ -380,7 +380,7 @@ def route_experts(logits, k: int, bias=None, score: str = "softmax", groups: int
     sptr = None if scores is None else _arg(scores, "scores", where, dev, (T, E),
                                             torch.float32)
     _run("sfn_route_experts", dev, stream, logits.data_ptr(), elt, bptr, eptr, wptr, sptr, T, E,
-         k, kind, groups, top_groups, group_top, 1 if renormalize else 0, scale)
+         k, kind, groups, top_groups, group_top, 1 if renormalize else 0, float(scale))
     return experts, weights, scores
 
 
@@ -405,7 +405,7 @@ def route_experts_backward(logits, experts, dweights, dscores=None, score: str =
     else:
         lptr = _arg(dlogits, "dlogits", where, dev, (T, E), logits.dtype)
     _run("sfn_route_experts_backward", dev, stream, logits.data_ptr(), elt, eptr, wptr, sptr,
-         lptr, T, E, k, kind, 1 if renormalize else 0, scale)
+         lptr, T, E, k, kind, 1 if renormalize else 0, float(scale))
     return dlogits
 
 
