@@ -1,0 +1,352 @@
+// route_backward.cu -- the gradient of routing (route.cuh).
+//
+// The gradient: with n_i = s_i / sum_j s_j,
+//   ds_i = scale (dw_i - sum_j dw_j n_j) / sum_j s_j (renormalised), or
+//   ds_i = scale dw_i; plus a dense ds (a balance loss on the scores)
+//   softmax: dl = s (ds - sum_e s_e ds_e);  sigmoid: dl = s (1 - s) ds
+#include "route.cuh"
+
+namespace sfn {
+namespace {
+
+struct RouteBwdParams {
+  const void *logits;
+  const int32_t *experts;
+  const float *dweights, *dscores;
+  void *dlogits;
+  int64_t T;
+  int E, k;
+  bool sigmoid, renorm;
+  float scale;
+};
+
+template <bool kBf16>
+__device__ __forceinline__ void store_grad(void *p, int64_t i, float g) {
+  if (kBf16)
+    static_cast<uint16_t *>(p)[i] = f32_to_bf16_bits(g);
+  else
+    static_cast<float *>(p)[i] = g;
+}
+
+__device__ __forceinline__ uint32_t pack_bf16x2(float lower, float upper) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(upper), "f"(lower));
+  return r;
+}
+
+// This lane's V gradients of row t.
+template <bool kBf16, int V, bool kBlocked, int kLanes = 32>
+__device__ __forceinline__ void store_row(void *out, int64_t t, int E, const float (&g)[V]) {
+  const int lane = threadIdx.x % kLanes;
+  if constexpr (kBlocked) {
+    constexpr int kBytes = V * (kBf16 ? 2 : 4);
+    uint32_t raw[kBytes / 4];
+#pragma unroll
+    for (int i = 0; i < kBytes / 4; ++i)
+      raw[i] = kBf16 ? pack_bf16x2(g[kBf16 ? 2 * i : i], g[kBf16 ? 2 * i + 1 : i])
+                     : __float_as_uint(g[kBf16 ? 0 : i]);
+    char *dst = static_cast<char *>(out) + (t * kLanes + lane) * kBytes;
+    if constexpr (kBytes >= 16) {
+#pragma unroll
+      for (int i = 0; i < kBytes / 16; ++i)
+        reinterpret_cast<uint4 *>(dst)[i] =
+            make_uint4(raw[4 * i], raw[4 * i + 1], raw[4 * i + 2], raw[4 * i + 3]);
+    } else if constexpr (kBytes == 8) {
+      *reinterpret_cast<uint2 *>(dst) = make_uint2(raw[0], raw[1]);
+    } else {
+      *reinterpret_cast<uint32_t *>(dst) = raw[0];
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < V; ++j)
+      if (lane + kLanes * j < E) store_grad<kBf16>(out, t * E + lane + kLanes * j, g[j]);
+  }
+}
+
+// Blocks of kWarps rows an SM holds at once.
+template <int V>
+constexpr int backward_blocks() {
+  return V <= 4 ? 10 : (V <= 8 ? 6 : (V <= 16 ? 4 : 2));
+}
+
+// One warp per row.
+// kDense: every score of the row is needed (softmax without renormalisation,
+// or a dscores): the slots' ds are added to the lanes' values in slot order,
+// and the row is written once.  Otherwise the gradient outside the chosen
+// experts is 0: for the renormalised softmax sum_e s_e ds_e = scale (sum_i dw_i
+// n_i - sum_j dw_j n_j sum_i n_i) / D = 0, and s_i / D needs the chosen logits
+// only; the row is written as zeros and, after a warp barrier that orders the
+// two, the chosen experts' gradients over it, lane i slot i's.
+template <bool kBf16, int V, bool kBlocked, bool kDense>
+__global__ void __launch_bounds__(32 * kWarps, backward_blocks<V>())
+    k_route_bwd(const RouteBwdParams p) {
+  pdl_wait();
+  pdl_launch_dependents();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t stride = (int64_t)gridDim.x * kWarps;
+  // the next row's inputs are on their way while this one is done
+  constexpr int kRow = kDense ? V : 1;
+  int next_e = -1;
+  float next_dw = 0.f, next_l[kRow], next_ds[kRow];
+  auto fetch = [&](int64_t t) {
+    if (lane < p.k) {
+      next_e = p.experts[t * p.k + lane];
+      next_dw = p.dweights[t * p.k + lane];
+    }
+    if constexpr (kDense) {
+      load_row<kBf16, V, kBlocked>(p.logits, t, p.E, next_l);
+      if (p.dscores != nullptr) load_row<false, V, kBlocked>(p.dscores, t, p.E, next_ds);
+    }
+  };
+  int64_t t = (int64_t)blockIdx.x * kWarps + warp;
+  if (t < p.T) fetch(t);
+  for (; t < p.T; t += stride) {
+    // lane i < k: slot i
+    const int e = next_e >= 0 && next_e < p.E ? next_e : -1;
+    const float dw = next_dw;
+    float le = -INFINITY, l[kRow], ds[kRow];
+    if (e >= 0) le = load_logit<kBf16>(p.logits, t * p.E + e);
+    if constexpr (kDense) {
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        l[j] = next_l[j];
+        ds[j] = p.dscores != nullptr ? next_ds[j] : 0.f;
+      }
+    }
+    if (t + stride < p.T) fetch(t + stride);
+    float m = 0.f, z = 1.f;
+    if (!p.sigmoid) {
+      if constexpr (kDense) {
+        // l becomes the row's scores
+        m = row_max<V>(l);
+        z = 0.f;
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+          l[j] = m == -INFINITY ? 0.f : expf(l[j] - m);
+          z += l[j];
+        }
+        z = warp_add(z);
+        const float inv = z == 0.f ? 0.f : 1.f / z;
+#pragma unroll
+        for (int j = 0; j < V; ++j) l[j] *= inv;
+      } else {
+        // only the ratio to the chosen experts' sum matters
+        const uint32_t key = __reduce_max_sync(kFull, e >= 0 ? order_key(le) : 0u);
+        m = key == 0u ? le : key_value(key);
+        if (m == -INFINITY) z = 0.f;
+      }
+    }
+    float d = p.scale * dw, s = 0.f;
+    if (p.renorm || !kDense) s = e >= 0 ? score_of<float>(le, p.sigmoid, m, z) : 0.f;
+    if (p.renorm) {
+      const float sum = warp_add(s);
+      const float mean = sum == 0.f ? 0.f : warp_add(dw * s) / sum;
+      d = sum == 0.f ? 0.f : p.scale * (dw - mean) / sum;
+    }
+    float g[V];
+    if constexpr (kDense) {
+      for (int i = 0; i < p.k; ++i) {
+        const int ei = __shfl_sync(kFull, e, i);
+        const float di = __shfl_sync(kFull, d, i);
+        // the owner lane and the value's place in it (-1: an empty slot, nobody)
+        const int at = ei < 0 ? -1 : (kBlocked ? ei - lane * V : ((ei & 31) == lane ? ei >> 5 : -1));
+#pragma unroll
+        for (int j = 0; j < V; ++j)
+          if (at == j) ds[j] += di;
+      }
+      if (!p.sigmoid) {
+        float dot = 0.f;
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+          // values past E have the score 0; their ds must not be -inf
+          if (!kBlocked && expert_of<V, kBlocked>(j) >= p.E) ds[j] = 0.f;
+          dot += l[j] * ds[j];
+        }
+        dot = warp_add(dot);
+#pragma unroll
+        for (int j = 0; j < V; ++j) g[j] = l[j] * (ds[j] - dot);
+      } else {
+        // 1 - sigma(l) = sigma(-l), without the cancellation
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+          const float x = expf(-fabsf(l[j])), q = 1.f / (1.f + x);
+          g[j] = ds[j] * (x * q) * q;
+        }
+      }
+      store_row<kBf16, V, kBlocked>(p.dlogits, t, p.E, g);
+    } else {
+#pragma unroll
+      for (int j = 0; j < V; ++j) g[j] = 0.f;
+      store_row<kBf16, V, kBlocked>(p.dlogits, t, p.E, g);
+      // the same expert in two slots: the first of them takes the sum
+      if (e < 0) d = 0.f;
+      bool first = e >= 0;
+      const uint32_t same = __match_any_sync(kFull, e >= 0 ? e : -1 - lane);
+      if (__any_sync(kFull, __popc(same) > 1)) {
+        float sum = 0.f;
+        for (int i = 0; i < p.k; ++i) {
+          const float di = __shfl_sync(kFull, d, i);
+          if ((same >> i) & 1u) sum += di;
+        }
+        d = sum;
+        first = first && __ffs(same) - 1 == lane;
+      }
+      __syncwarp();
+      if (first) {
+        float ge = s * d;
+        if (p.sigmoid) {
+          const float x = expf(-fabsf(le)), q = 1.f / (1.f + x);
+          ge = d * (x * q) * q;
+        }
+        store_grad<kBf16>(p.dlogits, t * p.E + e, ge);
+      }
+    }
+  }
+}
+
+// The dense form with eight lanes per row, four rows a warp, k <= 8, for many
+// rows (what does not depend on E is shared by four rows).  The rows are written
+// without their slots, then, after a warp barrier, each slot's whole gradient
+// over them by a lane of its own.
+template <bool kBf16, int V, bool kBlocked>
+__global__ void __launch_bounds__(32 * kWarps, lanes_blocks<V>())
+    k_route_bwd_lanes(const RouteBwdParams p) {
+  pdl_wait();
+  pdl_launch_dependents();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int sub = lane % kRowLanes, first = lane - sub;
+  const int64_t stride = (int64_t)gridDim.x * kWarps * 4;
+  for (int64_t t0 = ((int64_t)blockIdx.x * kWarps + warp) * 4; t0 < p.T; t0 += stride) {
+    const bool live = t0 + first / kRowLanes < p.T;
+    const int64_t t = live ? t0 + first / kRowLanes : p.T - 1;
+    float l[V], ds[V];
+    load_row<kBf16, V, kBlocked, kRowLanes>(p.logits, t, p.E, l);
+    if (p.dscores != nullptr) load_row<false, V, kBlocked, kRowLanes>(p.dscores, t, p.E, ds);
+    int e = -1;
+    float dw = 0.f, le = -INFINITY, de = 0.f;
+    if (sub < p.k) {
+      e = p.experts[t * p.k + sub];
+      dw = p.dweights[t * p.k + sub];
+      if (e < 0 || e >= p.E) e = -1;
+    }
+    if (e >= 0) {
+      le = load_logit<kBf16>(p.logits, t * p.E + e);
+      if (p.dscores != nullptr) de = __ldg(p.dscores + t * p.E + e);
+    }
+#pragma unroll
+    for (int j = 0; j < V; ++j)
+      // values past E have the score 0; their ds must not be -inf
+      if (p.dscores == nullptr || (!kBlocked && sub + kRowLanes * j >= p.E)) ds[j] = 0.f;
+    float s = 0.f;  // the slot's score
+    if (!p.sigmoid) {
+      float m = l[0];
+#pragma unroll
+      for (int j = 1; j < V; ++j) m = fmaxf(m, l[j]);
+      const uint32_t key = lanes_max(order_key(m));
+      m = key == 0u ? -INFINITY : key_value(key);
+      float z = 0.f;
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        l[j] = m == -INFINITY ? 0.f : expf(l[j] - m);  // l becomes the scores
+        z += l[j];
+      }
+      z = lanes_add(z);
+      const float inv = z == 0.f ? 0.f : 1.f / z;
+#pragma unroll
+      for (int j = 0; j < V; ++j) l[j] *= inv;
+      if (e >= 0 && m != -INFINITY) s = expf(le - m) * inv;
+    } else if (e >= 0) {
+      s = score_of<float>(le, true, 0.f, 1.f);
+    }
+    float d = p.scale * dw;
+    if (p.renorm) {
+      const float sum = lanes_add(s);
+      const float mean = sum == 0.f ? 0.f : lanes_add(dw * s) / sum;
+      d = sum == 0.f ? 0.f : p.scale * (dw - mean) / sum;
+    }
+    if (e < 0) d = 0.f;
+    const float mine = s * d;  // of the row's sum of s ds
+    // the same expert in two slots: the first of them takes the sum
+    bool store = e >= 0;
+    const uint32_t same = __match_any_sync(kFull, e >= 0 ? first / kRowLanes * p.E + e : -1 - lane);
+    if (__any_sync(kFull, __popc(same) > 1)) {
+      float sum = 0.f;
+      for (int i = 0; i < p.k; ++i) {
+        const float di = __shfl_sync(kFull, d, first + i);
+        if ((same >> (first + i)) & 1u) sum += di;
+      }
+      d = sum;
+      store = store && __ffs(same) - 1 == lane;
+    }
+    float g[V], ge;
+    if (!p.sigmoid) {
+      float dot = mine;
+#pragma unroll
+      for (int j = 0; j < V; ++j) dot += l[j] * ds[j];
+      dot = lanes_add(dot);
+#pragma unroll
+      for (int j = 0; j < V; ++j) g[j] = l[j] * (ds[j] - dot);
+      ge = s * (de + d - dot);
+    } else {
+      // 1 - sigma(l) = sigma(-l), without the cancellation
+      auto slope = [](float x) {
+        const float y = expf(-fabsf(x)), q = 1.f / (1.f + y);
+        return (y * q) * q;
+      };
+#pragma unroll
+      for (int j = 0; j < V; ++j) g[j] = ds[j] * slope(l[j]);
+      ge = (de + d) * slope(le);
+    }
+    if (live) store_row<kBf16, V, kBlocked, kRowLanes>(p.dlogits, t, p.E, g);
+    __syncwarp();
+    if (store && live) store_grad<kBf16>(p.dlogits, t * p.E + e, ge);
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_route_backward(const RouteShape &s, const void *logits,
+                                  const int32_t *experts, const float *dweights,
+                                  const float *dscores, void *dlogits, int num_sms,
+                                  cudaStream_t st) {
+  const RouteBwdParams p{logits, experts, dweights, dscores, dlogits, s.T,
+                         s.E,    s.k,     s.sigmoid, s.renorm, s.scale};
+  const bool dense = dscores != nullptr || (!s.sigmoid && !s.renorm);
+  const bool vectors = aligned16({logits, dscores, dlogits});
+  // Many rows: eight lanes each (32768 x 128 with dscores, bf16 10.7 us against
+  // 16.9, float32 14.0 against 16.1; 2048 x 64 3.1 against 2.7).
+  if (dense && s.T >= 8192 && s.k <= kRowLanes && s.E > 32 && s.E <= 256) {
+    auto go = [&](auto v) {
+      constexpr int V = decltype(v)::value;
+      auto launch = [&](auto *kern) {
+        return launch_rows(kern, (s.T + 3) / 4, lanes_blocks<V>(), 0, num_sms, st, p);
+      };
+      const bool blocked = vectors && s.E == kRowLanes * V;
+      if (s.bf16)
+        return blocked ? launch(k_route_bwd_lanes<true, V, true>)
+                       : launch(k_route_bwd_lanes<true, V, false>);
+      return blocked ? launch(k_route_bwd_lanes<false, V, true>)
+                     : launch(k_route_bwd_lanes<false, V, false>);
+    };
+    if (s.E <= 64) return go(std::integral_constant<int, 8>{});
+    if (s.E <= 128) return go(std::integral_constant<int, 16>{});
+    return go(std::integral_constant<int, 32>{});
+  }
+  return with_layout(s.E, vectors, false, [&](auto v, auto blocked) {
+    constexpr int V = decltype(v)::value;
+    constexpr bool kB = decltype(blocked)::value;
+    auto go = [&](auto bf16, auto all) {
+      if constexpr (kB && !vector_part<V>())  // (not reached, and not built)
+        return cudaErrorInvalidValue;
+      else
+        return launch_rows(k_route_bwd<decltype(bf16)::value, V, kB, decltype(all)::value>, s.T,
+                           backward_blocks<V>(), 0, num_sms, st, p);
+    };
+    auto with_all = [&](auto bf16) {
+      return dense ? go(bf16, std::true_type{}) : go(bf16, std::false_type{});
+    };
+    return s.bf16 ? with_all(std::true_type{}) : with_all(std::false_type{});
+  });
+}
+
+}  // namespace sfn
