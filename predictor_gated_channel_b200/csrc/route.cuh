@@ -32,9 +32,11 @@
 // What the rare paths cost is their latency, at the end of a launch: each
 // level (words, whole scores, float64 of the slots and the next two, float64 of
 // the row) is there so that few rows see the next.
-//   4096 x 256, 8 groups: 14.9 us; 22.5 us with whole keys alone (2557
-//   instructions a row), 20.9 us with float64 rows in place of float64 slots
-//   32768 x 160, bf16: 18.4 us (356 instructions a row); 38.9 us with whole keys
+//   4096 x 256, 8 groups: 11.0 us (of it 3 us of rows decided in float64); 22.5
+//   us with whole keys alone (2557 instructions a row), 20.9 us with float64 rows
+//   in place of float64 slots
+//   32768 x 160, bf16: 18.4 us (356 instructions a row), 13.0 us with eight lanes
+//   a row (route_lanes.cu); 38.9 us with whole keys
 #pragma once
 
 #include <cmath>
@@ -357,9 +359,11 @@ __device__ __forceinline__ float row_sum(const float (&l)[V], float m) {
 }
 
 // Blocks of kWarps rows an SM holds at once (the launch bound and the grid).
+// Seven for 256 experts, so that 4096 rows are one wave: 11.0 us; six, with the
+// next row's logits loaded ahead, 13.8 us.
 template <int V>
 constexpr int route_blocks() {
-  return V <= 4 ? 8 : (V <= 8 ? 6 : (V <= 16 ? 4 : 2));
+  return V <= 4 ? 8 : (V <= 8 ? 7 : (V <= 16 ? 4 : 2));
 }
 
 // Mask of a value's place among a lane's V, in the low bits of a packed word.

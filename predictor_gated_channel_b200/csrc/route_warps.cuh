@@ -23,14 +23,9 @@ __global__ void __launch_bounds__(32 * kWarps, route_blocks<V>()) k_route(const 
     }
   }
   const int64_t stride = (int64_t)gridDim.x * kWarps;
-  int64_t t = (int64_t)blockIdx.x * kWarps + warp;
-  float ahead[V];  // the next row's logits, on their way while this one is done
-  if (t < p.T) load_row<kBf16, V, kBlocked>(p.logits, t, p.E, ahead);
-  for (; t < p.T; t += stride) {
+  for (int64_t t = (int64_t)blockIdx.x * kWarps + warp; t < p.T; t += stride) {
     float l[V];
-#pragma unroll
-    for (int j = 0; j < V; ++j) l[j] = ahead[j];
-    if (t + stride < p.T) load_row<kBf16, V, kBlocked>(p.logits, t + stride, p.E, ahead);
+    load_row<kBf16, V, kBlocked>(p.logits, t, p.E, l);
     bool nan = false;
 #pragma unroll
     for (int j = 0; j < V; ++j) nan |= l[j] != l[j];
