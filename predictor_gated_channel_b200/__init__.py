@@ -25,9 +25,15 @@ __all__ = ["predict", "bank_topk", "sparse_ffn_forward", "dense4x_forward", "wor
            "experts_i8_workspace_bytes", "kernel_launch_count", "SfnError"]
 
 
+_module = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _module
+    if _module is None:
+        import torch
+        _module = torch
+    return _module
 
 
 def _stream_ptr(stream, device):
@@ -304,19 +310,22 @@ def _new(device, rows, cols, dtype):
     return _torch().empty_strided((rows, cols), (cols, 1), dtype=dtype, device=device)
 
 
-def _run(name, device, stream, *args):
-    """One C call on `stream` (default: the device's current one), with `device` current."""
-    cuda = _torch()._C
+def _raw_stream(device, stream):
+    return (_torch()._C._cuda_getCurrentRawStream(device.index) if stream is None
+            else stream.cuda_stream)
+
+
+def _run(name, device, args):
+    """One C call, its stream the last of `args`, with `device` current."""
     fn = _fns.get(name)
     if fn is None:
         fn = _fns[name] = getattr(_capi.lib(), name)
-    index = device.index
-    st = cuda._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
-    if cuda._cuda_getDevice() == index:
-        status = fn(*args, st)
+    torch = _torch()
+    if torch._C._cuda_getDevice() == device.index:
+        status = fn(*args)
     else:
-        with _torch().cuda.device(device):
-            status = fn(*args, st)
+        with torch.cuda.device(device):
+            status = fn(*args)
     if status:
         _capi.check(status, name)
 
@@ -333,9 +342,10 @@ def _scratch(workspace, nbytes, device):
 
 
 def _score(score):
-    if score not in SCORES:
+    kind = SCORES.get(score)
+    if kind is None:
         raise ValueError(f"score must be one of {sorted(SCORES)}")
-    return SCORES[score]
+    return kind
 
 
 def _matrix(t, name, where):
@@ -363,7 +373,7 @@ def route_experts(logits, k: int, bias=None, score: str = "softmax", groups: int
     where = "route_experts"
     T, E = _matrix(logits, "logits", where)
     dev = logits.device
-    elt, kind, slots = _kind(logits.dtype), _score(score), max(k, 0)
+    elt, kind, slots = _kind(logits.dtype), _score(score), k if k > 0 else 0
     bptr = None if bias is None else _arg(bias, "bias", where, dev, (E,), torch.float32)
     if experts is None:
         experts = _new(dev, T, slots, torch.int32)
@@ -379,8 +389,9 @@ def route_experts(logits, k: int, bias=None, score: str = "softmax", groups: int
         scores = _new(dev, T, E, torch.float32)
     sptr = None if scores is None else _arg(scores, "scores", where, dev, (T, E),
                                             torch.float32)
-    _run("sfn_route_experts", dev, stream, logits.data_ptr(), elt, bptr, eptr, wptr, sptr, T, E,
-         k, kind, groups, top_groups, group_top, 1 if renormalize else 0, float(scale))
+    _run("sfn_route_experts", dev,
+         (logits.data_ptr(), elt, bptr, eptr, wptr, sptr, T, E, k, kind, groups, top_groups,
+          group_top, 1 if renormalize else 0, float(scale), _raw_stream(dev, stream)))
     return experts, weights, scores
 
 
@@ -404,8 +415,9 @@ def route_experts_backward(logits, experts, dweights, dscores=None, score: str =
         lptr = dlogits.data_ptr()
     else:
         lptr = _arg(dlogits, "dlogits", where, dev, (T, E), logits.dtype)
-    _run("sfn_route_experts_backward", dev, stream, logits.data_ptr(), elt, eptr, wptr, sptr,
-         lptr, T, E, k, kind, 1 if renormalize else 0, float(scale))
+    _run("sfn_route_experts_backward", dev,
+         (logits.data_ptr(), elt, eptr, wptr, sptr, lptr, T, E, k, kind, 1 if renormalize else 0,
+          float(scale), _raw_stream(dev, stream)))
     return dlogits
 
 
@@ -425,8 +437,8 @@ def quantize_rows_i8(x, q=None, scale=None, stream=None):
         scale = torch.empty(lead, dtype=torch.float32, device=dev)
     qptr = _arg(q, "q", where, dev, x.shape, torch.int8)
     sptr = _arg(scale, "scale", where, dev, lead, torch.float32)
-    _run("sfn_quantize_rows_i8", dev, stream, x.data_ptr(), _elt(x.dtype), qptr, sptr,
-         scale.numel(), K)
+    _run("sfn_quantize_rows_i8", dev, (x.data_ptr(), _kind(x.dtype), qptr, sptr, scale.numel(), K,
+                                       _raw_stream(dev, stream)))
     return q, scale
 
 
@@ -446,7 +458,7 @@ def matmul_i8(xq, x_scale, wq, w_scale, out=None, out_dtype=None, stream=None):
             _arg(wq, "wq", where, dev, (N, K), torch.int8),
             _arg(w_scale, "w_scale", where, dev, (N,), torch.float32),
             _arg(out, "out", where, dev, (T, N), out_dtype or out.dtype)]
-    _run("sfn_matmul_i8", dev, stream, *ptrs, _kind(out.dtype), T, N, K)
+    _run("sfn_matmul_i8", dev, (*ptrs, _kind(out.dtype), T, N, K, _raw_stream(dev, stream)))
     return out
 
 
@@ -472,8 +484,8 @@ def linear_i8(x, wq, w_scale, out=None, out_dtype=None, workspace=None, stream=N
     else:
         yptr = _arg(out, "out", where, dev, (T, N), out_dtype or out.dtype)
     ws, nbytes, keep = _scratch(workspace, linear_i8_workspace_bytes(T, K), dev)
-    _run("sfn_linear_i8", dev, stream, x.data_ptr(), _kind(x.dtype), wptr, sptr, yptr,
-         _kind(out.dtype), T, N, K, ws, nbytes)
+    _run("sfn_linear_i8", dev, (x.data_ptr(), _kind(x.dtype), wptr, sptr, yptr, _kind(out.dtype), T,
+                                N, K, ws, nbytes, _raw_stream(dev, stream)))
     _used_on(keep, workspace, stream)
     return out
 
@@ -518,6 +530,7 @@ def experts_i8_forward(x, experts, weights, Wg, sg, Wu, su, Wd, sd, y=None, work
             _arg(Wd, "Wd", where, dev, (E, d, f), i8), _arg(sd, "sd", where, dev, (E, d), f32),
             _arg(y, "y", where, dev, (T, d), bf16)]
     ws, nbytes, keep = _scratch(workspace, experts_i8_workspace_bytes(T, E, k, d, f), dev)
-    _run("sfn_experts_i8_forward", dev, stream, *ptrs, T, E, k, d, f, ws, nbytes)
+    _run("sfn_experts_i8_forward", dev,
+         (*ptrs, T, E, k, d, f, ws, nbytes, _raw_stream(dev, stream)))
     _used_on(keep, workspace, stream)
     return y
