@@ -4,8 +4,8 @@
 namespace sfn {
 namespace {
 
-// Eight lanes a row instead of a warp: 32768 x 160 bf16 13.0 us against 18.4,
-// 8192 x 64 3.6 against 6.1, 2048 x 160 3.0 against 3.2; float32 32768 x 160 17.0
+// Eight lanes a row instead of a warp: 32768 x 160 bf16 11.5 us against 18.4,
+// 8192 x 64 3.6 against 6.1, 2048 x 160 3.0 against 3.2; float32 32768 x 160 13.3
 // against 24.1.  With a bias, where rows may be left to the whole warp, for many
 // rows only: 32768 x 64 20.8 us against 30.0, but 4096 x 256 in groups 15.6
 // against 11.0.

@@ -35,7 +35,7 @@
 //   4096 x 256, 8 groups: 11.0 us (of it 3 us of rows decided in float64); 22.5
 //   us with whole keys alone (2557 instructions a row), 20.9 us with float64 rows
 //   in place of float64 slots
-//   32768 x 160, bf16: 18.4 us (356 instructions a row), 13.0 us with eight lanes
+//   32768 x 160, bf16: 18.4 us (356 instructions a row), 11.5 us with eight lanes
 //   a row (route_lanes.cu); 38.9 us with whole keys
 #pragma once
 
@@ -372,10 +372,14 @@ constexpr uint32_t places() {
   return V <= 1 ? 0u : V <= 2 ? 1u : V <= 4 ? 3u : V <= 8 ? 7u : V <= 16 ? 15u : 31u;
 }
 
-// As route_blocks(), of k_route_lanes.
-template <int V>
+// As route_blocks(), of the kernels with eight lanes a row.  Seven of 16 values
+// make 32768 rows two rounds of the warps in place of three (128 experts, bf16:
+// 10.9 to 9.6 us for the gradient); with more values only the kernels that need
+// few registers gain (160 experts by logit 14.6 to 11.5 us; the gradient of 256
+// would spill, 8.9 to 9.5).
+template <int V, bool kFewRegisters>
 constexpr int lanes_blocks() {
-  return V <= 8 ? 8 : (V <= 16 ? 6 : 4);
+  return V <= 8 ? 8 : (V <= 16 || kFewRegisters ? 7 : 4);
 }
 
 // Among a row's eight lanes.

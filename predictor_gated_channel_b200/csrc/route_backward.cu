@@ -209,7 +209,7 @@ __global__ void __launch_bounds__(32 * kWarps, backward_blocks<V>())
 // without their slots, then, after a warp barrier, each slot's whole gradient
 // over them by a lane of its own.
 template <bool kBf16, int V, bool kBlocked>
-__global__ void __launch_bounds__(32 * kWarps, lanes_blocks<V>())
+__global__ void __launch_bounds__(32 * kWarps, (lanes_blocks<V, false>()))
     k_route_bwd_lanes(const RouteBwdParams p) {
   pdl_wait();
   pdl_launch_dependents();
@@ -313,13 +313,13 @@ cudaError_t launch_route_backward(const RouteShape &s, const void *logits,
                          s.E,    s.k,     s.sigmoid, s.renorm, s.scale};
   const bool dense = dscores != nullptr || (!s.sigmoid && !s.renorm);
   const bool vectors = aligned16({logits, dscores, dlogits});
-  // Many rows: eight lanes each (32768 x 128 with dscores, bf16 10.7 us against
-  // 16.9, float32 14.0 against 16.1; 2048 x 64 3.1 against 2.7).
+  // Many rows: eight lanes each (32768 x 128 with dscores, bf16 9.6 us against
+  // 16.9, float32 12.3 against 16.1; 2048 x 64 3.1 against 2.7).
   if (dense && s.T >= 8192 && s.k <= kRowLanes && s.E > 32 && s.E <= 256) {
     auto go = [&](auto v) {
       constexpr int V = decltype(v)::value;
       auto launch = [&](auto *kern) {
-        return launch_rows(kern, (s.T + 3) / 4, lanes_blocks<V>(), 0, num_sms, st, p);
+        return launch_rows(kern, (s.T + 3) / 4, lanes_blocks<V, false>(), 0, num_sms, st, p);
       };
       const bool blocked = vectors && s.E == kRowLanes * V;
       if (s.bf16)

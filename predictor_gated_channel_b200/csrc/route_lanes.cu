@@ -61,7 +61,7 @@ __device__ __forceinline__ void top8(const uint32_t (&w)[V], uint32_t (&top)[8])
 // anything to settle (a NaN, neighbours or a k-th place within the words or the
 // error bound, more than eight of one lane) is left to the whole warp.
 template <bool kBf16, int V, bool kByLogit, bool kGroups>
-__global__ void __launch_bounds__(32 * kWarps, lanes_blocks<V>())
+__global__ void __launch_bounds__(32 * kWarps, (lanes_blocks<V, kByLogit>()))
     k_route_lanes(const RouteParams p) {
   extern __shared__ double route_smem[];
   pdl_wait();
@@ -255,7 +255,7 @@ cudaError_t launch_route_lanes(const RouteParams &p, bool by_logit, int num_sms,
     auto launch = [&](auto logit, auto grouped) {
       return launch_rows(
           k_route_lanes<kBf16, V, decltype(logit)::value, decltype(grouped)::value>,
-          (p.T + 3) / 4, lanes_blocks<V>(), smem, num_sms, st, p);
+          (p.T + 3) / 4, lanes_blocks<V, decltype(logit)::value>(), smem, num_sms, st, p);
     };
     if (groups) return launch(std::true_type{}, std::true_type{});
     return by_logit ? launch(std::true_type{}, std::false_type{})
