@@ -630,13 +630,16 @@ __device__ __forceinline__ int select_row(const RouteParams &p, int64_t t, const
       if (!kByLogit && p.bias != nullptr) bp = __ldg(p.bias + pick);
     }
   };
-  bool unsure = nan || !packed;
-  if (!unsure) {
-    float c[V];
+  float c[V];
+  bool number = true;  // the words have no room for a NaN (of l, of a bias, of exp(inf - inf))
 #pragma unroll
-    for (int j = 0; j < V; ++j)
-      c[j] = kByLogit ? l[j]
-                      : select_score(score_fast(l[j], p.sigmoid, m, z_fast), l[j], bias[j]);
+  for (int j = 0; j < V; ++j) {
+    c[j] = kByLogit ? l[j]
+                    : select_score(score_fast(l[j], p.sigmoid, m, z_fast), l[j], bias[j]);
+    if (!kByLogit) number &= c[j] == c[j];
+  }
+  bool unsure = nan || !packed || (!kByLogit && !__all_sync(kFull, number));
+  if (!unsure) {
     // the largest score there can be, for the error bounds
     const float most = p.sigmoid || kByLogit ? 1.f : (z_fast > 0.f ? __fdividef(1.f, z_fast) : 0.f);
     bool in = true;  // this lane's group stays

@@ -108,13 +108,16 @@ __global__ void __launch_bounds__(32 * kWarps, (lanes_blocks<V, kByLogit>()))
       z = m == -INFINITY ? 0.f : lanes_add(b);
     }
     float c[V];
+    bool number = true;  // the words have no room for a NaN (of a bias, of exp(inf - inf))
 #pragma unroll
-    for (int j = 0; j < V; ++j)
+    for (int j = 0; j < V; ++j) {
       c[j] = kByLogit ? l[j]
                       : select_score(score_fast(l[j], p.sigmoid, m, z_fast), l[j], bias[j]);
+      if (!kByLogit) number &= c[j] == c[j];
+    }
     const float most = p.sigmoid || kByLogit ? 1.f : (z_fast > 0.f ? __fdividef(1.f, z_fast) : 0.f);
     auto bound = [&](float x) { return score_error(most, x, p.sigmoid); };
-    bool unsure = nan, in = true;
+    bool unsure = nan || (!kByLogit && !number), in = true;
     if (kGroups) {
       float a = -INFINITY, b = -INFINITY;
 #pragma unroll
@@ -237,9 +240,10 @@ __global__ void __launch_bounds__(32 * kWarps, (lanes_blocks<V, kByLogit>()))
       weight = sum == 0.f ? 0.f : weight / sum;
     }
     if (slot && live) {
+      const bool bad = !p.sigmoid && (nan || m == INFINITY);  // as in k_route
       p.experts[t * p.k + sub] = empty ? -1 : pick;
       p.weights[t * p.k + sub] =
-          empty ? 0.f : (nan && !p.sigmoid ? __int_as_float(0x7fc00000) : weight * p.scale);
+          empty ? 0.f : (bad ? __int_as_float(0x7fc00000) : weight * p.scale);
     }
   }
 }

@@ -65,10 +65,11 @@ __global__ void __launch_bounds__(32 * kWarps, route_blocks<V>()) k_route(const 
       w = sum == 0.f ? 0.f : w / sum;
     }
     if (slot) {
-      // a NaN anywhere makes the softmax, and with it every weight, NaN
+      // a NaN or +inf anywhere makes the softmax, and with it every weight, NaN
+      const bool bad = !p.sigmoid && (nan || m == INFINITY);
       p.experts[t * p.k + lane] = empty ? -1 : pick;
       p.weights[t * p.k + lane] =
-          empty ? 0.f : (nan && !p.sigmoid ? __int_as_float(0x7fc00000) : w * p.scale);
+          empty ? 0.f : (bad ? __int_as_float(0x7fc00000) : w * p.scale);
     }
   }
 }

@@ -213,6 +213,31 @@ def test_route_scores_a_rounding_apart(E, groups, score):
     assert np.array_equal(e.cpu().numpy(), re)
 
 
+def test_route_biases_that_are_no_numbers():
+    """A NaN bias ranks its expert below every number, +inf above, -inf takes it
+    out; a softmax row with +inf has NaN scores, which rank equal: the lower
+    indexes.  In rows few and many (other kernels), with and without groups."""
+    E, k = 64, 4
+    for T, groups, top in ((7, 1, 1), (7, 8, 8), (20000, 1, 1)):
+        logits = rand(3, T, E)
+        bias = torch.zeros(E)
+        bias[5], bias[9], bias[11], bias[60] = math.nan, math.inf, -math.inf, math.inf
+        for score in ("softmax", "sigmoid"):
+            e, w, _ = sfn.route_experts(logits.to(DEV), k, bias=bias.to(DEV), score=score,
+                                        groups=groups, top_groups=top)
+            ok = bias.clone()
+            ok[5] = -math.inf    # below every number: not among four of 62
+            re, rw, _ = ref_route(logits[:50], k, ok, score, groups, top)
+            assert np.array_equal(e.cpu()[:50].numpy(), re)
+            assert (e[:, 0] == 9).all() and (e[:, 1] == 60).all()
+            assert np.allclose(w.cpu()[:50].double().numpy(), rw, rtol=100 * U, atol=1e-37)
+        logits[2, 7] = math.inf
+        e, w, _ = sfn.route_experts(logits.to(DEV), k, bias=torch.zeros(E, device=DEV),
+                                    groups=groups, top_groups=top)
+        assert e[2].tolist() == [0, 1, 2, 3] and torch.isnan(w[2]).all()
+        assert torch.isfinite(w[[0, 1, 3, 4, 5, 6]]).all()
+
+
 @pytest.mark.parametrize("E", [5, 64, 160, 256, 600])
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 def test_route_backward_long(E, dtype):
