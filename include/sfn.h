@@ -311,6 +311,12 @@ sfn_status sfn_sparse_ffn_backward(const void *x, const void *A, const void *B, 
                                    sfn_stream_t stream);
 
 /*
+ * The operators of whole experts, from here to sfn_experts_i8_forward: an
+ * output or workspace must not overlap an input (rows are read again after
+ * others have been written).
+ */
+
+/*
  * Routing of tokens to experts: which k of E experts a token goes to, and
  * with which weights.  For a token's logits l [E]:
  *   s = softmax(l) (SFN_SCORE_SOFTMAX) or 1 / (1 + exp(-l)) (SFN_SCORE_SIGMOID)

@@ -310,9 +310,16 @@ def _new(device, rows, cols, dtype):
     return _torch().empty_strided((rows, cols), (cols, 1), dtype=dtype, device=device)
 
 
-def _raw_stream(device, stream):
-    return (_torch()._C._cuda_getCurrentRawStream(device.index) if stream is None
-            else stream.cuda_stream)
+def _raw_stream(device):
+    return _torch()._C._cuda_getCurrentRawStream(device.index)
+
+
+def _on(stream, device, where):
+    """`stream` as the current one: what a call allocates then belongs to it.
+    (Memory from another stream's pool may still have work pending there.)"""
+    if stream.device != device:
+        raise ValueError(f"{where}: the stream is on {stream.device}, not on {device}")
+    return _torch().cuda.stream(stream)
 
 
 def _run(name, device, args):
@@ -373,6 +380,10 @@ def route_experts(logits, k: int, bias=None, score: str = "softmax", groups: int
     where = "route_experts"
     T, E = _matrix(logits, "logits", where)
     dev = logits.device
+    if stream is not None:
+        with _on(stream, dev, where):
+            return route_experts(logits, k, bias, score, groups, top_groups, group_top, renormalize,
+                                 scale, experts, weights, scores, want_scores)
     elt, kind, slots = _kind(logits.dtype), _score(score), k if k > 0 else 0
     bptr = None if bias is None else _arg(bias, "bias", where, dev, (E,), torch.float32)
     if experts is None:
@@ -391,7 +402,7 @@ def route_experts(logits, k: int, bias=None, score: str = "softmax", groups: int
                                             torch.float32)
     _run("sfn_route_experts", dev,
          (logits.data_ptr(), elt, bptr, eptr, wptr, sptr, T, E, k, kind, groups, top_groups,
-          group_top, 1 if renormalize else 0, float(scale), _raw_stream(dev, stream)))
+          group_top, 1 if renormalize else 0, float(scale), _raw_stream(dev)))
     return experts, weights, scores
 
 
@@ -404,6 +415,10 @@ def route_experts_backward(logits, experts, dweights, dscores=None, score: str =
     where = "route_experts_backward"
     T, E = _matrix(logits, "logits", where)
     dev = logits.device
+    if stream is not None:
+        with _on(stream, dev, where):
+            return route_experts_backward(logits, experts, dweights, dscores, score, renormalize,
+                                          scale, dlogits)
     elt, kind = _kind(logits.dtype), _score(score)
     k = _matrix(experts, "experts", where)[1]
     eptr = _arg(experts, "experts", where, dev, (T, k), torch.int32)
@@ -417,7 +432,7 @@ def route_experts_backward(logits, experts, dweights, dscores=None, score: str =
         lptr = _arg(dlogits, "dlogits", where, dev, (T, E), logits.dtype)
     _run("sfn_route_experts_backward", dev,
          (logits.data_ptr(), elt, eptr, wptr, sptr, lptr, T, E, k, kind, 1 if renormalize else 0,
-          float(scale), _raw_stream(dev, stream)))
+          float(scale), _raw_stream(dev)))
     return dlogits
 
 
@@ -431,6 +446,9 @@ def quantize_rows_i8(x, q=None, scale=None, stream=None):
     if x.dim() < 1:
         raise ValueError(f"{where}: x must have a dimension")
     dev, lead, K = x.device, x.shape[:-1], x.shape[-1]
+    if stream is not None:
+        with _on(stream, dev, where):
+            return quantize_rows_i8(x, q, scale)
     if q is None:
         q = torch.empty(x.shape, dtype=torch.int8, device=dev)
     if scale is None:
@@ -438,7 +456,7 @@ def quantize_rows_i8(x, q=None, scale=None, stream=None):
     qptr = _arg(q, "q", where, dev, x.shape, torch.int8)
     sptr = _arg(scale, "scale", where, dev, lead, torch.float32)
     _run("sfn_quantize_rows_i8", dev, (x.data_ptr(), _kind(x.dtype), qptr, sptr, scale.numel(), K,
-                                       _raw_stream(dev, stream)))
+                                       _raw_stream(dev)))
     return q, scale
 
 
@@ -451,6 +469,9 @@ def matmul_i8(xq, x_scale, wq, w_scale, out=None, out_dtype=None, stream=None):
     T, K = _matrix(xq, "xq", where)
     N = _matrix(wq, "wq", where)[0]
     dev = xq.device
+    if stream is not None:
+        with _on(stream, dev, where):
+            return matmul_i8(xq, x_scale, wq, w_scale, out, out_dtype)
     if out is None:
         out = _new(dev, T, N, out_dtype or torch.bfloat16)
     ptrs = [_arg(xq, "xq", where, dev, (T, K), torch.int8),
@@ -458,7 +479,7 @@ def matmul_i8(xq, x_scale, wq, w_scale, out=None, out_dtype=None, stream=None):
             _arg(wq, "wq", where, dev, (N, K), torch.int8),
             _arg(w_scale, "w_scale", where, dev, (N,), torch.float32),
             _arg(out, "out", where, dev, (T, N), out_dtype or out.dtype)]
-    _run("sfn_matmul_i8", dev, (*ptrs, _kind(out.dtype), T, N, K, _raw_stream(dev, stream)))
+    _run("sfn_matmul_i8", dev, (*ptrs, _kind(out.dtype), T, N, K, _raw_stream(dev)))
     return out
 
 
@@ -476,6 +497,9 @@ def linear_i8(x, wq, w_scale, out=None, out_dtype=None, workspace=None, stream=N
     T, K = _matrix(x, "x", where)
     N = _matrix(wq, "wq", where)[0]
     dev = x.device
+    if stream is not None:
+        with _on(stream, dev, where):
+            return linear_i8(x, wq, w_scale, out, out_dtype, workspace)
     wptr = _arg(wq, "wq", where, dev, (N, K), torch.int8)
     sptr = _arg(w_scale, "w_scale", where, dev, (N,), torch.float32)
     if out is None:
@@ -483,17 +507,10 @@ def linear_i8(x, wq, w_scale, out=None, out_dtype=None, workspace=None, stream=N
         yptr = out.data_ptr()
     else:
         yptr = _arg(out, "out", where, dev, (T, N), out_dtype or out.dtype)
-    ws, nbytes, keep = _scratch(workspace, linear_i8_workspace_bytes(T, K), dev)
+    ws, nbytes, _keep = _scratch(workspace, linear_i8_workspace_bytes(T, K), dev)
     _run("sfn_linear_i8", dev, (x.data_ptr(), _kind(x.dtype), wptr, sptr, yptr, _kind(out.dtype), T,
-                                N, K, ws, nbytes, _raw_stream(dev, stream)))
-    _used_on(keep, workspace, stream)
+                                N, K, ws, nbytes, _raw_stream(dev)))
     return out
-
-
-def _used_on(scratch, given, stream):
-    """Scratch taken here must not be reused by the allocator before `stream` is done."""
-    if given is None and stream is not None:
-        scratch.record_stream(stream)
 
 
 @functools.lru_cache(maxsize=4096)
@@ -515,6 +532,9 @@ def experts_i8_forward(x, experts, weights, Wg, sg, Wu, su, Wd, sd, y=None, work
     T, d = _matrix(x, "x", where)
     _, k = _matrix(experts, "experts", where)
     dev = x.device
+    if stream is not None:
+        with _on(stream, dev, where):
+            return experts_i8_forward(x, experts, weights, Wg, sg, Wu, su, Wd, sd, y, workspace)
     _dev(Wg, "Wg")
     if Wg.dim() != 3:
         raise ValueError(f"{where}: Wg must be [E, f, d]")
@@ -529,8 +549,7 @@ def experts_i8_forward(x, experts, weights, Wg, sg, Wu, su, Wd, sd, y=None, work
             _arg(Wu, "Wu", where, dev, (E, f, d), i8), _arg(su, "su", where, dev, (E, f), f32),
             _arg(Wd, "Wd", where, dev, (E, d, f), i8), _arg(sd, "sd", where, dev, (E, d), f32),
             _arg(y, "y", where, dev, (T, d), bf16)]
-    ws, nbytes, keep = _scratch(workspace, experts_i8_workspace_bytes(T, E, k, d, f), dev)
+    ws, nbytes, _keep = _scratch(workspace, experts_i8_workspace_bytes(T, E, k, d, f), dev)
     _run("sfn_experts_i8_forward", dev,
-         (*ptrs, T, E, k, d, f, ws, nbytes, _raw_stream(dev, stream)))
-    _used_on(keep, workspace, stream)
+         (*ptrs, T, E, k, d, f, ws, nbytes, _raw_stream(dev)))
     return y

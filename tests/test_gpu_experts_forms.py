@@ -312,6 +312,30 @@ def test_two_streams_at_once():
         assert torch.equal(z1, y1) and torch.equal(z2, y2)
 
 
+def test_memory_of_another_stream_is_not_taken():
+    """A block freed while its own stream still writes it must not become the
+    output or scratch of a call on another stream."""
+    T, N, K = 64, 4096, 4096
+    x = rand(1, T, K).to(torch.bfloat16).to(DEV)
+    wq, sw = (t.to(DEV) for t in weights_i8(5, N, K))
+    want = sfn.linear_i8(x, wq, sw)
+    logits = rand(2, 5000, 64).to(DEV)
+    e0, w0, _ = sfn.route_experts(logits, 8)
+    side = torch.cuda.Stream()
+    for _ in range(5):
+        blocks = [torch.empty_like(want), torch.empty_like(e0), torch.empty_like(w0),
+                  torch.empty(sfn.linear_i8_workspace_bytes(T, K), dtype=torch.uint8, device=DEV)]
+        torch.cuda.synchronize()
+        torch.cuda._sleep(4_000_000)   # about 2 ms
+        for b in blocks:
+            b.fill_(7)
+        del blocks, b
+        y = sfn.linear_i8(x, wq, sw, stream=side)
+        e, w, _ = sfn.route_experts(logits, 8, stream=side)
+        torch.cuda.synchronize()
+        assert torch.equal(y, want) and torch.equal(e, e0) and torch.equal(w, w0)
+
+
 def test_weights_written_just_before():
     """Weights quantised on the stream right before the call that reads them:
     the product must not run ahead of them."""
