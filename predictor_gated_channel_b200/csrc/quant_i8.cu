@@ -9,8 +9,10 @@
 // with an infinity or a NaN has scale NaN and q 0, so that everything
 // computed from it is NaN.
 //
-// kRowWarps warps per row hold the row in registers between the maximum and
-// the quantisation (one read of x); longer rows are read again (from L2).
+// kRowWarps warps per row hold it in registers, kHeld 16-byte chunks a thread,
+// between the maximum and the quantisation (one read of x); longer rows are read
+// again (from L2).  Short rows have kernels of their own: the unrolled chunks that
+// they do not have would cost as much as theirs.
 #include "async_util.cuh"
 #include "experts.cuh"
 #include "quant_i8.cuh"
@@ -19,7 +21,6 @@ namespace sfn {
 namespace {
 
 constexpr int kQuantWarps = 8;  // per block
-constexpr int kHeld = 8;        // 16-byte chunks a thread holds
 
 // Source rows -> destination rows of one launch.
 struct QuantParams {
@@ -33,8 +34,8 @@ struct QuantParams {
   int copies;
 };
 
-template <class Elt, int kRowWarps>
-__global__ void __launch_bounds__(32 * kQuantWarps, 4) k_quantize_rows(const QuantParams p) {
+template <class Elt, int kRowWarps, int kHeld>
+__global__ void __launch_bounds__(32 * kQuantWarps, kHeld <= 2 ? 8 : 4) k_quantize_rows(const QuantParams p) {
   constexpr int kThreads = 32 * kRowWarps;       // per row
   constexpr int kRows = kQuantWarps / kRowWarps;  // per block
   __shared__ uint32_t part[kQuantWarps];
@@ -101,11 +102,14 @@ cudaError_t launch(const QuantParams &p, int num_sms, cudaStream_t st) {
     return launch_pdl(kern, dim3((unsigned)(blocks < most ? blocks : most)),
                       dim3(32 * kQuantWarps), 0, st, p);
   };
-  // the fewest warps that hold a row in registers
-  if (chunks <= 32 * kHeld) return go(k_quantize_rows<Elt, 1>, 1);
-  if (chunks <= 64 * kHeld) return go(k_quantize_rows<Elt, 2>, 2);
-  if (chunks <= 128 * kHeld) return go(k_quantize_rows<Elt, 4>, 4);
-  return go(k_quantize_rows<Elt, 8>, 8);
+  // the fewest warps and chunks that hold a row in registers
+  if (chunks <= 32) return go(k_quantize_rows<Elt, 1, 1>, 1);
+  if (chunks <= 64) return go(k_quantize_rows<Elt, 1, 2>, 1);
+  if (chunks <= 128) return go(k_quantize_rows<Elt, 1, 4>, 1);
+  if (chunks <= 256) return go(k_quantize_rows<Elt, 1, 8>, 1);
+  if (chunks <= 512) return go(k_quantize_rows<Elt, 2, 8>, 2);
+  if (chunks <= 1024) return go(k_quantize_rows<Elt, 4, 8>, 4);
+  return go(k_quantize_rows<Elt, 8, 8>, 8);
 }
 
 }  // namespace

@@ -10,7 +10,7 @@ namespace {
 // rows only: 32768 x 64 20.8 us against 30.0, but 4096 x 256 in groups 15.6
 // against 11.0.
 bool by_lanes(const RouteParams &p, bool by_logit) {
-  if (p.k > 8 || p.scores != nullptr || p.E <= 32 || p.E > 256) return false;
+  if (p.k > 8 || p.scores != nullptr || p.E > 256) return false;
   if (p.groups > 1)  // a lane's values are neighbours, as many as are built
     return by_logit && p.T >= 2048 && 8 % p.groups == 0 && aligned16({p.logits}) &&
            (p.E == 64 || p.E == 128 || p.E == 160 || p.E == 256);

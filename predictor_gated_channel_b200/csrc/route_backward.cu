@@ -315,7 +315,7 @@ cudaError_t launch_route_backward(const RouteShape &s, const void *logits,
   const bool vectors = aligned16({logits, dscores, dlogits});
   // Many rows: eight lanes each (32768 x 128 with dscores, bf16 9.6 us against
   // 16.9, float32 12.3 against 16.1; 2048 x 64 3.1 against 2.7).
-  if (dense && s.T >= 8192 && s.k <= kRowLanes && s.E > 32 && s.E <= 256) {
+  if (dense && s.T >= 8192 && s.k <= kRowLanes && s.E <= 256) {
     auto go = [&](auto v) {
       constexpr int V = decltype(v)::value;
       auto launch = [&](auto *kern) {

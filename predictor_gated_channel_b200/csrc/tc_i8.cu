@@ -769,17 +769,29 @@ cudaError_t launch_i8_gemm(const I8Shape &s, const DeviceInfo &dev, const int8_t
 }
 
 namespace {
-// Tiles of the grouped products.  How many rows an expert has is known on the
-// device only; the tile is as wide as twice the average asks for, so that a
-// decode batch does not pay for a prefill's stages.  Pairs from 64 rows an
-// expert on: of 64 experts of 4096 x 1792, 512 rows each, 934 us against 958
-// with one CTA a tile, 128 rows 372 against 379, but 32 rows 298 against 294
-// and 8 rows 255 against 250.
-constexpr int kPairRows = 64;
-Tiling grouped_tiling(const ExpertShape &s) {
-  const int64_t twice = 2 * s.slots() / s.E + 16;
-  const bool pair = s.slots() >= (int64_t)s.E * kPairRows;
-  return tile_rows(twice < 256 ? twice : 256, 256, pair, true);
+// Tiles of a grouped product (n channels an expert, k long, num_w matrices).
+// How many rows an expert has is known on the device only; with few on average
+// the tile is as wide as twice the average asks for, so that a decode batch does
+// not pay for a prefill's stages and seldom reads an expert's weights twice.
+// With 64 and more, pairs of 256 rows where they run long and fill the SMs one
+// and a half times: of 64 experts of 4096 x 1792, 128 rows each, 323 us against
+// 332 (SwiGLU) and 347 (down) with one CTA a tile; but single CTAs of 128 rows
+// (SwiGLU) or 256 (down), or of 64 where those would not fill half of the SMs, for
+// short products and few tiles: 64 experts of 576 x 416, 150 rows, 77 against 82
+// us; 8 of 2048 x 1024, 128 rows, 42 against 46; 2 of 1712 x 224, 960 rows, 36
+// against 43.
+Tiling grouped_tiling(const ExpertShape &s, int n, int k, int num_w, int num_sms) {
+  const int64_t slots = s.slots(), rows = slots / s.E;
+  if (rows < 32) return tile_rows(2 * rows + 16, 256, false, true);
+  if (rows < 64) return tile_rows(num_w == 2 ? 64 : 2 * rows + 16, 256, false, true);
+  auto tiles = [&](int bn, int channels) {  // about: an expert's last tile is half full
+    const int64_t used = slots < s.E ? slots : s.E;
+    return used * (2 * rows + bn) / (2 * bn) * ((n + channels - 1) / channels);
+  };
+  const int slices = (k + kSliceK - 1) / kSliceK;
+  if (slices >= 8 && 4 * tiles(256, 2 * kTileN) >= 3 * num_sms) return tile_rows(256, 256, true, true);
+  const int wide = num_w == 2 ? 128 : 256;
+  return tile_rows(2 * tiles(wide, kTileN) >= num_sms ? wide : 64, 256, false, true);
 }
 template <bool kSwiGlu, Out kOut>
 cudaError_t launch_grouped(const CUtensorMap &mX, const CUtensorMap &mW, const CUtensorMap &mW2,
@@ -794,7 +806,7 @@ cudaError_t launch_i8_experts_gateup(const ExpertShape &s, const DeviceInfo &dev
                                      const int32_t *offsets, const int8_t *xq, const float *sx,
                                      const int8_t *Wg, const float *sg, const int8_t *Wu,
                                      const float *su, uint16_t *h, cudaStream_t st) {
-  const Tiling t = grouped_tiling(s);
+  const Tiling t = grouped_tiling(s, s.f, s.d, 2, dev.num_sms);
   I8Params p = params(t, s.f, s.d, 2, dev.err);
   p.rows = s.slots();
   p.offsets = offsets;
@@ -816,7 +828,7 @@ cudaError_t launch_i8_experts_down(const ExpertShape &s, const DeviceInfo &dev,
                                    const int32_t *offsets, const int8_t *hq, const int8_t *Wd,
                                    const float *sd, uint16_t *o, uint8_t *exponents,
                                    cudaStream_t st) {
-  const Tiling t = grouped_tiling(s);
+  const Tiling t = grouped_tiling(s, s.d, s.f, 1, dev.num_sms);
   I8Params p = params(t, s.d, s.f, 1, dev.err);
   p.rows = s.slots();
   p.offsets = offsets;
