@@ -261,7 +261,8 @@ __global__ void __launch_bounds__(32 * kWarps, (lanes_blocks<V, false>()))
     float d = p.scale * dw;
     if (p.renorm) {
       const float sum = lanes_add(s);
-      const float mean = sum == 0.f ? 0.f : lanes_add(dw * s) / sum;
+      const float dot = lanes_add(dw * s);  // by all lanes: the rows of a warp differ in sum
+      const float mean = sum == 0.f ? 0.f : dot / sum;
       d = sum == 0.f ? 0.f : p.scale * (dw - mean) / sum;
     }
     if (e < 0) d = 0.f;

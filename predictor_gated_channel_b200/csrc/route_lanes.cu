@@ -104,8 +104,11 @@ __global__ void __launch_bounds__(32 * kWarps, (lanes_blocks<V, kByLogit>()))
         if (!kByLogit) a += __expf(l[j] - m);
         if (!p.renorm) b += expf(l[j] - m);
       }
-      z_fast = m == -INFINITY ? 0.f : lanes_add(a);
-      z = m == -INFINITY ? 0.f : lanes_add(b);
+      // the sums by all lanes: the rows of a warp differ in m
+      a = lanes_add(a);
+      b = lanes_add(b);
+      z_fast = m == -INFINITY ? 0.f : a;
+      z = m == -INFINITY ? 0.f : b;
     }
     float c[V];
     bool number = true;  // the words have no room for a NaN (of a bias, of exp(inf - inf))

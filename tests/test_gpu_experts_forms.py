@@ -14,7 +14,7 @@ import predictor_gated_channel_b200 as sfn
 from predictor_gated_channel_b200 import _capi
 from predictor_gated_channel_b200 import build as sfn_build
 from test_gpu_experts import (BF16, DEV, U, expert_weights, rand, ref_experts, ref_quantize,
-                              ref_route, weights_i8)
+                              ref_route, ref_route_bwd, weights_i8)
 
 pytestmark = pytest.mark.gpu
 
@@ -257,6 +257,61 @@ def test_route_backward_long(E, dtype):
     if dtype == torch.bfloat16:
         tol = tol + BF16 * ref.abs()
     assert ((got - ref).abs() <= tol).all()
+
+
+@pytest.mark.parametrize("T,E,k,groups,top,bias", [
+    (5000, 5, 3, 1, 1, False), (5000, 25, 6, 1, 1, False), (17000, 9, 2, 1, 1, True),
+    (17000, 250, 8, 1, 1, True), (3000, 250, 8, 1, 1, False), (3000, 160, 8, 8, 4, False),
+    (3001, 64, 4, 4, 2, False), (2050, 256, 8, 2, 1, False), (4099, 130, 1, 1, 1, False),
+])
+@pytest.mark.parametrize("grid", [True, False])
+def test_route_many_rows(T, E, k, groups, top, bias, grid):
+    """Eight lanes a row: lanes without values, odd row counts, ties (on a grid)
+    and plain values, with masked rows among them."""
+    g = torch.Generator().manual_seed(T + E)
+    logits = torch.randn((T, E), generator=g) * 1.5
+    if grid:
+        logits = torch.round(logits * 8) / 8
+    logits[7] = -math.inf
+    logits[11, 1:] = -math.inf
+    b = torch.round(torch.randn(E, generator=g) * 4) / 64 if bias else None
+    rows = torch.cat([torch.arange(100), torch.arange(T - 60, T)])
+    for dtype in (torch.float32, torch.bfloat16):
+        x = logits.to(dtype)
+        for score in ("softmax", "sigmoid"):
+            for renorm in (True, False):
+                e, w, _ = sfn.route_experts(x.to(DEV), k, bias=None if b is None else b.to(DEV),
+                                            score=score, groups=groups, top_groups=top,
+                                            renormalize=renorm, scale=1.5)
+                re, rw, _ = ref_route(x[rows], k, b, score, groups, top, 1, renorm, 1.5)
+                assert np.array_equal(e.cpu()[rows].numpy(), re)
+                assert np.allclose(w.cpu()[rows].double().numpy(), rw, rtol=100 * U, atol=1e-37)
+
+
+@pytest.mark.parametrize("T,E,k", [(9001, 5, 3), (8192, 64, 8), (9000, 100, 4), (8195, 128, 8),
+                                   (8200, 256, 5)])
+@pytest.mark.parametrize("score,renorm", [("softmax", False), ("softmax", True),
+                                          ("sigmoid", True)])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_route_backward_many_rows(T, E, k, score, renorm, dtype):
+    g = torch.Generator().manual_seed(E)
+    logits = torch.randn((T, E), generator=g).to(dtype)
+    experts = torch.topk(logits.float(), k, dim=1).indices.to(torch.int32)
+    experts[::7, k - 1] = -1
+    experts[3::9, 1] = experts[3::9, 0]     # the same expert twice
+    dw, ds = torch.randn((T, k), generator=g), torch.randn((T, E), generator=g)
+    got = sfn.route_experts_backward(logits.to(DEV), experts.to(DEV), dw.to(DEV),
+                                     dscores=ds.to(DEV), score=score, renormalize=renorm,
+                                     scale=1.5)
+    ref, s = ref_route_bwd(logits, experts, dw, ds, score, renorm, 1.5)
+    chosen = (s.gather(1, experts.long().clamp(min=0)) * (experts >= 0)).sum(1, keepdim=True)
+    unit = 1.5 * dw.abs().double().amax(1, keepdim=True) * 2
+    if renorm:
+        unit = unit / chosen.clamp(min=1e-30)
+    # as in test_route_backward: terms of at most max |ds| each, right to 100 u
+    unit = unit + 2 * ds.abs().double().amax(1, keepdim=True)
+    tol = 100 * U * unit * s + (BF16 * ref.abs() if dtype == torch.bfloat16 else 0) + 1e-37
+    assert ((got.cpu().double() - ref).abs() <= tol).all()
 
 
 # ------------------------------------------------------- as a program calls them
