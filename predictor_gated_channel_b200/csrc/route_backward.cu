@@ -103,7 +103,7 @@ __global__ void __launch_bounds__(32 * kWarps, backward_blocks<V>())
   for (; t < p.T; t += stride) {
     // lane i < k: slot i
     const int e = next_e >= 0 && next_e < p.E ? next_e : -1;
-    const float dw = next_dw;
+    const float dw = e >= 0 ? next_dw : 0.f;  // an empty slot's says nothing
     float le = -INFINITY, l[kRow], ds[kRow];
     if (e >= 0) le = load_logit<kBf16>(p.logits, t * p.E + e);
     if constexpr (kDense) {
@@ -139,9 +139,14 @@ __global__ void __launch_bounds__(32 * kWarps, backward_blocks<V>())
     float d = p.scale * dw, s = 0.f;
     if (p.renorm || !kDense) s = e >= 0 ? score_of<float>(le, p.sigmoid, m, z) : 0.f;
     if (p.renorm) {
+      // dw_i - sum_j dw_j n_j on the differences from one slot's dw: the sum of
+      // the n is 1, and what all slots have in common (for k = 1 everything)
+      // then cancels exactly
+      const int ref = __ffs(__ballot_sync(kFull, e >= 0)) - 1;
+      const float by = dw - __shfl_sync(kFull, dw, ref < 0 ? 0 : ref);
       const float sum = warp_add(s);
-      const float mean = sum == 0.f ? 0.f : warp_add(dw * s) / sum;
-      d = sum == 0.f ? 0.f : p.scale * (dw - mean) / sum;
+      const float mean = sum == 0.f ? 0.f : warp_add(by * s) / sum;
+      d = sum == 0.f ? 0.f : p.scale * (by - mean) / sum;
     }
     float g[V];
     if constexpr (kDense) {
@@ -227,7 +232,10 @@ __global__ void __launch_bounds__(32 * kWarps, (lanes_blocks<V, false>()))
     if (sub < p.k) {
       e = p.experts[t * p.k + sub];
       dw = p.dweights[t * p.k + sub];
-      if (e < 0 || e >= p.E) e = -1;
+      if (e < 0 || e >= p.E) {
+        e = -1;
+        dw = 0.f;
+      }
     }
     if (e >= 0) {
       le = load_logit<kBf16>(p.logits, t * p.E + e);
@@ -261,9 +269,12 @@ __global__ void __launch_bounds__(32 * kWarps, (lanes_blocks<V, false>()))
     float d = p.scale * dw;
     if (p.renorm) {
       const float sum = lanes_add(s);
-      const float dot = lanes_add(dw * s);  // by all lanes: the rows of a warp differ in sum
+      // as in k_route_bwd; by all lanes: the rows of a warp differ in sum
+      const uint32_t used = __ballot_sync(kFull, e >= 0) & (0xffu << first);
+      const float by = dw - __shfl_sync(kFull, dw, used == 0u ? first : __ffs(used) - 1);
+      const float dot = lanes_add(by * s);
       const float mean = sum == 0.f ? 0.f : dot / sum;
-      d = sum == 0.f ? 0.f : p.scale * (dw - mean) / sum;
+      d = sum == 0.f ? 0.f : p.scale * (by - mean) / sum;
     }
     if (e < 0) d = 0.f;
     const float mine = s * d;  // of the row's sum of s ds

@@ -314,6 +314,28 @@ def test_route_backward_many_rows(T, E, k, score, renorm, dtype):
     assert ((got.cpu().double() - ref).abs() <= tol).all()
 
 
+@pytest.mark.parametrize("T", [50, 9000])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_route_backward_of_constant_weights(T, score):
+    """Renormalised weights do not change where there is one expert, nor along
+    a dweights that is the same for all slots: gradients of exactly 0.  What an
+    empty slot's dweights holds does not matter."""
+    E = 100
+    logits = rand(T, T, E)
+    for k in (1, 4):
+        experts = torch.topk(logits, k, dim=1).indices.to(torch.int32)
+        dw = rand(3, T, 1).repeat(1, k)
+        experts[5] = -1
+        dw[5] = math.nan
+        if k > 1:
+            experts[::3, 0] = -1
+            dw[::3, 0] = math.inf
+        for ds in (None, torch.zeros((T, E))):
+            g = sfn.route_experts_backward(logits.to(DEV), experts.to(DEV), dw.to(DEV), score=score,
+                                           dscores=None if ds is None else ds.to(DEV))
+            assert (g == 0).all()
+
+
 # ------------------------------------------------------- as a program calls them
 def test_captured_and_replayed():
     """Every form of the product in one graph, with one workspace, replayed on
