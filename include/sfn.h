@@ -403,7 +403,9 @@ sfn_status sfn_linear_i8(const void *x, sfn_dtype x_dtype, const int8_t *wq,
  * for slot i of token t with expert e = experts[t][i] and weight w,
  *   g = Wg[e] x_t,  u = Wu[e] x_t        (products as in sfn_linear_i8)
  *   h = silu(g) u, rounded to bf16, then quantised as a row of its own
- *   y_t = sum_i w_i (Wd[e] h_i), summed in float32, rounded to bf16
+ *   y_t = sum_i w_i (Wd[e] h_i), products and sum in float32, in slot order,
+ *         rounded once, to bf16
+ * A token's result is the same, bit for bit, whatever tokens share the call.
  * x, y bf16 [T][d]; experts int32 and weights float32 [T][k] as
  * sfn_route_experts gives them (a slot of -1 adds nothing; an expert may be
  * in several slots; an index >= E adds nothing and sets bit 2 of the device

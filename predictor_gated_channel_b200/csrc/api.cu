@@ -973,8 +973,7 @@ sfn_status sfn_experts_i8_forward(const void *x, const int32_t *experts, const f
   uint16_t *h = reinterpret_cast<uint16_t *>(w + p.off_h);
   int8_t *hq = reinterpret_cast<int8_t *>(w + p.off_hq);
   float *sh = reinterpret_cast<float *>(w + p.off_sh);
-  uint16_t *o = reinterpret_cast<uint16_t *>(w + p.off_o);
-  uint8_t *exponents = reinterpret_cast<uint8_t *>(w + p.off_exp);
+  float *o = reinterpret_cast<float *>(w + p.off_o);
   cudaError_t e = cudaSuccess;
   auto step = [&](int stage, auto &&launch) {
     if (e == cudaSuccess) e = timed(stage, st, launch);
@@ -999,10 +998,9 @@ sfn_status sfn_experts_i8_forward(const void *x, const int32_t *experts, const f
   step(SFN_STAGE_I8_ROWS,
        [&] { return launch_quantize_expert_rows(s, h, offsets, hq, sh, dev.num_sms, st); });
   step(SFN_STAGE_I8_PRODUCT,
-       [&] { return launch_i8_experts_down(s, dev, offsets, hq, Wd, sd, o, exponents, st); });
+       [&] { return launch_i8_experts_down(s, dev, offsets, hq, sh, Wd, sd, o, st); });
   step(SFN_STAGE_I8_ROWS, [&] {
-    return launch_expert_combine(s, o, exponents, pos, experts, sh, weights,
-                                 static_cast<uint16_t *>(y), st);
+    return launch_expert_combine(s, o, pos, weights, static_cast<uint16_t *>(y), st);
   });
   return cuda_status(e);
 }

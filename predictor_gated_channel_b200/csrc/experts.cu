@@ -9,8 +9,6 @@
 #include "experts.cuh"
 #include "quant_i8.cuh"
 
-#include <cuda_fp16.h>
-
 namespace sfn {
 namespace {
 
@@ -80,32 +78,25 @@ __global__ void __launch_bounds__(kPlanThreads)
 // y_t = sum over the slots, in slot order and float32; a thread has 8 channels.
 // Bound by the reads of o; the loads of four slots are issued together.
 __global__ void __launch_bounds__(kCombineThreads)
-    k_expert_combine(const uint16_t *__restrict__ o, const uint8_t *__restrict__ exponents,
-                     const int32_t *__restrict__ pos, const int32_t *__restrict__ experts,
-                     const float *__restrict__ sh, const float *__restrict__ weights,
-                     uint16_t *__restrict__ y, int k, int d, float inv_unit) {
+    k_expert_combine(const float *__restrict__ o, const int32_t *__restrict__ pos,
+                     const float *__restrict__ weights, uint16_t *__restrict__ y, int k, int d) {
   pdl_wait();
   pdl_launch_dependents();
   const int64_t t = blockIdx.x;
   const int c = (blockIdx.y * kCombineThreads + threadIdx.x) * 8;
   if (c >= d) return;
-  const int blocks = (d + 31) / 32;
   float s[8] = {};
 #pragma unroll 4
   for (int i = 0; i < k; ++i) {
     const int64_t at = t * k + i;
     const int r = pos[at];
     if (r < 0) continue;
-    const uint4 v = ld_stream16(o + (int64_t)r * d + c);
-    const uint32_t eb = exponents[(int64_t)experts[at] * blocks + c / 32];
-    const float f = weights[at] * (sh[r] * inv_unit) * __uint_as_float(eb << 23);
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    const float *src = o + (int64_t)r * d + c;
+    const uint4 a = ld_stream16(src), b = ld_stream16(src + 4);
+    const float w = weights[at];
+    const uint32_t v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const float2 h = __half22float2(*reinterpret_cast<const __half2 *>(&w[j]));
-      s[2 * j] += f * h.x;
-      s[2 * j + 1] += f * h.y;
-    }
+    for (int j = 0; j < 8; ++j) s[j] = __fmaf_rn(w, __uint_as_float(v[j]), s[j]);
   }
   uint32_t out[4];
 #pragma unroll
@@ -133,8 +124,7 @@ ExpertPlan plan_experts(const ExpertShape &s) {
   p.off_h = take(R * s.f * 2);
   p.off_hq = take(R * s.f);
   p.off_sh = take(R * 4);
-  p.off_o = take(R * s.d * 2);
-  p.off_exp = take((size_t)s.E * ((s.d + 31) / 32));
+  p.off_o = take(R * s.d * 4);
   p.total = off;
   return p;
 }
@@ -146,15 +136,12 @@ cudaError_t launch_expert_plan(const ExpertShape &s, const int32_t *experts, int
                     s.slots(), s.E, err);
 }
 
-cudaError_t launch_expert_combine(const ExpertShape &s, const uint16_t *o,
-                                  const uint8_t *exponents, const int32_t *pos,
-                                  const int32_t *experts, const float *sh, const float *weights,
-                                  uint16_t *y, cudaStream_t st) {
+cudaError_t launch_expert_combine(const ExpertShape &s, const float *o, const int32_t *pos,
+                                  const float *weights, uint16_t *y, cudaStream_t st) {
   const unsigned parts = (unsigned)((s.d + 8 * kCombineThreads - 1) / (8 * kCombineThreads));
   count_launches(1);
   return launch_pdl(k_expert_combine, dim3((unsigned)s.T, parts), dim3(kCombineThreads), 0, st, o,
-                    exponents, pos, experts, sh, weights, y, s.k, s.d,
-                    1.f / expert_out_unit(s.f));
+                    pos, weights, y, s.k, s.d);
 }
 
 }  // namespace sfn

@@ -4,7 +4,7 @@
 //   k_linear_gemv    y[t][n] = sx[t] sw[n] sum_k xq[t][k] wq[n][k], x quantised
 //                    in the kernel
 //   k_experts_gateup h[s][c] = bf16(silu(g) u) for the slots s = (t, i)
-//   k_experts_down   y[t][n] = sum_i w[t][i] sh[s] sd[e][n] sum_c hq[s][c] Wd[e][n][c],
+//   k_experts_down   y[t][n] = sum_i w[t][i] (sum_c hq[s][c] Wd[e][n][c]) sh[s] sd[e][n],
 //                    h quantised in the kernel
 //
 // With so few tokens a product is a stream of weight rows and nothing else, so
@@ -35,7 +35,7 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kPiece = 2048;  // most bytes of a row per bulk copy
 constexpr int kStages = 2;    // pieces in flight per warp
 constexpr int kHeldX = 2;     // 16-byte chunks of x a thread holds
-constexpr size_t kSmemMost = 232448 - 1024;  // of 227 KB: room for the static arrays
+constexpr size_t kSmemMost = 232448 - 1280;  // of 227 KB: room for the static arrays
 
 // Rows [0, rows) of x (length K, contiguous) quantised into xq [rows][K] with
 // their scales, by all threads of the block: load() starts the reads of a
@@ -399,7 +399,7 @@ __global__ void __launch_bounds__(kThreads)
     const float a = sx[s / k];
     const float2 w = scale[i];
     const float g = (float)acc[2 * i] * a * w.x, up = (float)acc[2 * i + 1] * a * w.y;
-    h[u] = ids[s] < 0 ? (uint16_t)0 : f32_to_bf16_bits(g * sigmoid_f32(g) * up);
+    h[u] = ids[s] < 0 ? (uint16_t)0 : f32_to_bf16_bits(swiglu_f32(g, up));
   }
 }
 
@@ -417,6 +417,7 @@ __global__ void __launch_bounds__(kThreads)
   __shared__ float sh[kGemvSlots];
   __shared__ uint32_t amax[kGemvSlots];
   __shared__ int ids[kGemvSlots];
+  __shared__ float slot_weight[kGemvSlots];
   init_bars(bars);
   const int slots = T * k;
   int u0, u1;
@@ -428,6 +429,7 @@ __global__ void __launch_bounds__(kThreads)
   if (threadIdx.x < slots) {
     const int e = experts[threadIdx.x];
     ids[threadIdx.x] = (e >= 0 && e < E) ? e : -1;
+    slot_weight[threadIdx.x] = weights[threadIdx.x];
   }
   if (threadIdx.x < kGemvSlots) amax[threadIdx.x] = 0u;
   __syncthreads();
@@ -436,7 +438,7 @@ __global__ void __launch_bounds__(kThreads)
         for (int i = threadIdx.x; i < units * k; i += kThreads) {
           const int u = u0 + i / k, s = u / d * k + i % k;
           acc[i] = 0;
-          scale[i] = ids[s] >= 0 ? weights[s] * sd[(int64_t)ids[s] * d + u % d] : 0.f;
+          scale[i] = ids[s] >= 0 ? sd[(int64_t)ids[s] * d + u % d] : 0.f;
         }
         pdl_wait();
         pdl_launch_dependents();
@@ -450,7 +452,9 @@ __global__ void __launch_bounds__(kThreads)
     const int u = u0 + i, t = u / d;
     float s = 0.f;
     for (int j = 0; j < k; ++j)
-      if (ids[t * k + j] >= 0) s += (float)acc[i * k + j] * (sh[t * k + j] * scale[i * k + j]);
+      if (ids[t * k + j] >= 0)
+        s = __fmaf_rn(slot_weight[t * k + j],
+                      (float)acc[i * k + j] * sh[t * k + j] * scale[i * k + j], s);
     y[u] = f32_to_bf16_bits(s);
   }
 }

@@ -39,7 +39,6 @@
 #include "tc_util.cuh"
 
 #include <cudaTypedefs.h>
-#include <cuda_fp16.h>
 
 #include <type_traits>
 
@@ -47,9 +46,8 @@ namespace sfn {
 namespace {
 
 enum class Span { kOne, kPair, kSplit };
-// What the scaled product is stored as.  kBlockHalf: without the row's scale,
-// in fp16 with a power of two for each 32 channels (see block_scale).
-enum class Out { kF32, kBF16, kBlockHalf };
+// What the scaled product is stored as.
+enum class Out { kF32, kBF16 };
 
 constexpr int kTileN = 128;                    // output channels per CTA (UMMA M, half of a pair's)
 constexpr int kSliceK = 128;                   // K bytes per stage
@@ -75,8 +73,6 @@ struct I8Params {
   bool early;              // the weights and offsets are there before the previous kernel's end
   const float *sx, *sw, *sw2;
   void *out;               // [rows][n]
-  uint8_t *exponents;      // kBlockHalf: [groups][ceil(n / 32)]
-  float unit;              // kBlockHalf: a power of two, at most 1 / K
   unsigned *err;
 };
 
@@ -273,19 +269,6 @@ __device__ __forceinline__ auto out_value(float y) {
     return y;
 }
 
-// The experts' outputs before their weighted sum: half the bytes of float32
-// (they are the largest traffic of a prefill), rounded to 11 bits, an eighth
-// of the step of the bf16 sum.  The accumulator times unit (<= 1 / K) is below
-// 127^2; times sw over its block's power of two, below 4 * 127^2 < 65504, so
-// nothing overflows, and a channel loses bits to the range only where its scale
-// is below 2^-10 of its block's largest.  The exponent of the largest finite
-// |sw| of this warp's 32 channels:
-__device__ __forceinline__ int block_exponent(float sw) {
-  const uint32_t bits = __float_as_uint(sw) & 0x7fffffffu;
-  const uint32_t most = __reduce_max_sync(kFull, bits < 0x7f800000u ? bits : 0u);
-  return min(max((int)(most >> 23), 1), 253);
-}
-
 template <bool kSwiGlu, Out kOut, Span kSpan>
 __global__ void __launch_bounds__((block_threads<kSwiGlu, kSpan>()), 1)
     k_i8_gemm(const __grid_constant__ CUtensorMap tX, const __grid_constant__ CUtensorMap tW,
@@ -465,18 +448,12 @@ __global__ void __launch_bounds__((block_threads<kSwiGlu, kSpan>()), 1)
       const int ch = t.ch0 + (kPair ? (int)rank * kTileN : 0) + q * 32 + lane;
       const bool valid = ch < p.n;
       const int64_t wch = (int64_t)t.g * p.n + ch;
-      float sw = valid ? __ldg(p.sw + wch) : 0.f;
+      const float sw = valid ? __ldg(p.sw + wch) : 0.f;
       const float sw2 = (kSwiGlu && valid) ? __ldg(p.sw2 + wch) : 0.f;
-      if constexpr (kOut == Out::kBlockHalf) {
-        const int eb = block_exponent(sw);
-        if (lane == 0 && valid)
-          p.exponents[(int64_t)t.g * ((p.n + 31) / 32) + ch / 32] = (uint8_t)eb;
-        sw *= __int_as_float((254 - eb) << 23) * p.unit;
-      }
       // the rows' scales, before the wait for the tile
       const int rows = t.row1 - t.row0;
       float sx[kEpiChunks];
-      if constexpr (!kSplit && kOut != Out::kBlockHalf) {
+      if constexpr (!kSplit) {
 #pragma unroll
         for (int j = 0; j < kEpiChunks; ++j) {
           const int r = 32 * (part + j * kEpiParts) + lane;
@@ -526,12 +503,7 @@ __global__ void __launch_bounds__((block_threads<kSwiGlu, kSpan>()), 1)
           if constexpr (kSwiGlu) {
             const float a = __shfl_sync(kFull, sx[j], i);
             const float g = x * a * sw, up = (float)(int)u[i] * a * sw2;
-            // silu(g) up, rounded once to bf16: the element type the FFN's
-            // activations have in this library, and what is requantised.  The
-            // fast exponential and quotient are good to a few units of 2^-24.
-            return bf16_bits(__fdividef(g, 1.f + __expf(-g)) * up);
-          } else if constexpr (kOut == Out::kBlockHalf) {
-            return __half_as_ushort(__float2half_rn(x * sw));
+            return bf16_bits(swiglu_f32(g, up));
           } else {
             return out_value<kOut>(x * __shfl_sync(kFull, sx[j], i) * sw);
           }
@@ -825,8 +797,8 @@ cudaError_t launch_i8_experts_gateup(const ExpertShape &s, const DeviceInfo &dev
 }
 
 cudaError_t launch_i8_experts_down(const ExpertShape &s, const DeviceInfo &dev,
-                                   const int32_t *offsets, const int8_t *hq, const int8_t *Wd,
-                                   const float *sd, uint16_t *o, uint8_t *exponents,
+                                   const int32_t *offsets, const int8_t *hq, const float *sh,
+                                   const int8_t *Wd, const float *sd, float *o,
                                    cudaStream_t st) {
   const Tiling t = grouped_tiling(s, s.d, s.f, 1, dev.num_sms);
   I8Params p = params(t, s.d, s.f, 1, dev.err);
@@ -834,15 +806,14 @@ cudaError_t launch_i8_experts_down(const ExpertShape &s, const DeviceInfo &dev,
   p.offsets = offsets;
   p.groups = s.E;
   p.early = true;
+  p.sx = sh;
   p.sw = sd;
   p.out = o;
-  p.exponents = exponents;
-  p.unit = expert_out_unit(s.f);
   CUtensorMap mX, mW;
   if (!map_i8(&mX, hq, (uint64_t)s.f, (uint64_t)s.slots(), (uint32_t)p.box) ||
       !map_i8(&mW, Wd, (uint64_t)s.f, (uint64_t)s.E * s.d, kTileN))
     return cudaErrorInvalidValue;
-  return launch_grouped<false, Out::kBlockHalf>(mX, mW, mW, t, p, dev.num_sms, st);
+  return launch_grouped<false, Out::kF32>(mX, mW, mW, t, p, dev.num_sms, st);
 }
 
 }  // namespace sfn
