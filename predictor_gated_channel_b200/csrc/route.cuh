@@ -284,6 +284,10 @@ __device__ __forceinline__ void pick_packed(uint32_t (&w)[V], int k0, int k, uin
 //   (below 20u for up to 1024 terms) and 37 roundings; the quotient 4u:
 //   below 80u s + 8u
 // and c = s + b adds u |c|.
+// Decisions are tested as !(difference > bound), so that what is no number counts
+// as undecided: the difference of two infinities (of biases, of a sum of two that
+// passed the range), and the bound that a packed word of +inf gives, whose place
+// bits make it a NaN.
 constexpr float kUlp = 5.9604645e-8f;
 __device__ __forceinline__ float score_error(float s, float c, bool sigmoid) {
   return kUlp * ((sigmoid ? 0.f : 80.f * s) + 8.f + fabsf(c));
@@ -468,14 +472,14 @@ __device__ __noinline__ int settle_row(const RouteParams &p, int64_t t, double *
       // equal logits with equal biases are in the right order already
       const bool tie = l0 == l1 && b0 == b1;
       bool unsure = lane < p.k && c0 > -INFINITY && c1 > -INFINITY && !tie &&
-                    c0 - c1 <= score_error(s0, c0, p.sigmoid) + score_error(s1, c1, p.sigmoid);
+                    !(c0 - c1 > score_error(s0, c0, p.sigmoid) + score_error(s1, c1, p.sigmoid));
       // at the end of the order a third value could hide behind a tie
       if (lane == p.k - 1 && tie && c1 > -INFINITY) unsure = true;
-      if (lo > -INFINITY && hi > -INFINITY && lo < INFINITY) {
+      if (lo > -INFINITY && hi > -INFINITY) {
         // a group's score sums at most two, each at most the largest score
         const float s = p.sigmoid ? 1.f : (z > 0.f ? __fdividef(1.f, z) : 0.f);
-        unsure |= lo - hi <= 2.f * (score_error(s, lo, p.sigmoid) + score_error(s, hi, p.sigmoid)) +
-                                 4.f * kUlp * (fabsf(lo) + fabsf(hi));
+        unsure |= !(lo - hi > 2.f * (score_error(s, lo, p.sigmoid) + score_error(s, hi, p.sigmoid)) +
+                                  4.f * kUlp * (fabsf(lo) + fabsf(hi)));
       }
       if (!__any_sync(kFull, unsure)) return pick;
     }
@@ -672,10 +676,10 @@ __device__ __forceinline__ int select_row(const RouteParams &p, int64_t t, const
         // places?  First by the words (32 units of the last place apart),
         // then by the whole scores.  A group's score sums at most two.
         auto close = [&](float lo, float hi) {
-          return kByLogit ? lo <= hi
-                          : lo - hi <= 2.f * (score_error(most, lo, p.sigmoid) +
-                                              score_error(most, hi, p.sigmoid)) +
-                                           4.f * kUlp * (fabsf(lo) + fabsf(hi));
+          return kByLogit ? !(lo > hi)
+                          : !(lo - hi > 2.f * (score_error(most, lo, p.sigmoid) +
+                                               score_error(most, hi, p.sigmoid)) +
+                                            4.f * kUlp * (fabsf(lo) + fabsf(hi)));
         };
         if (close(key_value(last & ~31u), key_value(left | 31u))) {
           const uint32_t key = number_key(gs);
@@ -725,7 +729,7 @@ __device__ __forceinline__ int select_row(const RouteParams &p, int64_t t, const
       uint32_t left = __reduce_max_sync(kFull, w[0]);
       bool rest = left != 0u && (left & ~low) != (none & ~low);
       if constexpr (kByLogit) {
-        unsure |= lane == p.k - 1 && rest && cp <= key_value(left | low);
+        unsure |= lane == p.k - 1 && rest && !(cp > key_value(left | low));
       } else {
         auto bound = [&](float c) { return score_error(most, c, p.sigmoid); };
         const float l1 = __shfl_down_sync(kFull, lp, 1), b1 = __shfl_down_sync(kFull, bp, 1);
@@ -733,10 +737,10 @@ __device__ __forceinline__ int select_row(const RouteParams &p, int64_t t, const
         if (slot && cp > -INFINITY) {
           if (lane == p.k - 1) {
             const float hi = key_value(left | low);
-            close = rest && cp - hi <= bound(cp) + bound(hi);
+            close = rest && !(cp - hi > bound(cp) + bound(hi));
           } else {  // equal logits with equal biases are in the right order
             close = c1 > -INFINITY && !(lp == l1 && bp == b1) &&
-                    cp - c1 <= bound(cp) + bound(c1);
+                    !(cp - c1 > bound(cp) + bound(c1));
           }
         }
         if (!__any_sync(kFull, unsure) && __any_sync(kFull, close)) {
@@ -763,7 +767,7 @@ __device__ __forceinline__ int select_row(const RouteParams &p, int64_t t, const
             exchange_sort(kx, lane, 0, c64, pick, lp, bp);
           const double last = __shfl_sync(kFull, c64, p.k - 1);
           const float hi = key_value(left | low);
-          unsure = rest && (float)last - hi <= bound(hi) + 2.f * kUlp * fabsf(hi);
+          unsure = rest && !((float)last - hi > bound(hi) + 2.f * kUlp * fabsf(hi));
         }
       }
     }

@@ -200,14 +200,15 @@ __global__ void __launch_bounds__(32 * kWarps, (lanes_blocks<V, kByLogit>()))
       const bool rest = left != 0u && (left & ~low) != (none & ~low);
       const float hi = key_value(left | low);
       if constexpr (kByLogit) {
-        unsure |= sub == p.k - 1 && rest && cp <= hi;
+        unsure |= sub == p.k - 1 && rest && !(cp > hi);
       } else {
         const float l1 = __shfl_down_sync(kFull, lp, 1), b1 = __shfl_down_sync(kFull, bp, 1);
         if (slot && cp > -INFINITY) {
           if (sub == p.k - 1)
-            unsure |= rest && cp - hi <= bound(cp) + bound(hi);
+            unsure |= rest && !(cp - hi > bound(cp) + bound(hi));
           else
-            unsure |= c1 > -INFINITY && !(lp == l1 && bp == b1) && cp - c1 <= bound(cp) + bound(c1);
+            unsure |= c1 > -INFINITY && !(lp == l1 && bp == b1) &&
+                      !(cp - c1 > bound(cp) + bound(c1));
         }
       }
     }

@@ -12,7 +12,7 @@ import torch
 import predictor_gated_channel_b200 as sfn
 from predictor_gated_channel_b200 import _capi
 from predictor_gated_channel_b200 import build as sfn_build
-from test_gpu_experts import DEV, expert_weights, rand
+from test_gpu_experts import DEV, expert_weights, rand, ref_route
 
 pytestmark = pytest.mark.gpu
 
@@ -42,3 +42,70 @@ def test_experts_token_by_itself(T, E, k, d, f):
         part = sfn.experts_i8_forward(x[rows].contiguous(), experts[rows].contiguous(),
                                       weights[rows].contiguous(), **W)
         assert torch.equal(part, y[rows]), (first, n)
+
+
+# ------------------------------------------------------------------- choices
+def offset_view(t, by):
+    """The same values `by` elements into an allocation: no 16-byte loads."""
+    buf = torch.empty(t.numel() + by, dtype=t.dtype, device=t.device)
+    view = buf[by:].view(t.shape)
+    view.copy_(t)
+    return view
+
+
+@pytest.mark.parametrize("where", ["logits", "bias"])
+@pytest.mark.parametrize("T,E,groups,top", [
+    (200, 64, 1, 1), (200, 128, 1, 1), (200, 256, 1, 1), (200, 512, 1, 1), (200, 1024, 1, 1),
+    (200, 96, 1, 1), (200, 64, 8, 5), (200, 160, 8, 5), (200, 192, 4, 3), (200, 256, 8, 5),
+    (200, 384, 16, 9), (200, 100, 5, 3), (2100, 64, 1, 1), (2100, 256, 1, 1), (2100, 64, 4, 3),
+    (2100, 160, 8, 5), (2100, 256, 2, 2), (16500, 64, 1, 1), (16500, 250, 1, 1),
+])
+def test_route_infinite_ties(T, E, groups, top, where):
+    """More +inf logits (or biases) than slots: equal ones to the lower index,
+    wherever they lie among a lane's values and in any batch and alignment."""
+    g = torch.Generator().manual_seed(T + E)
+    rows = torch.cat([torch.arange(120), torch.arange(T - 60, T)])
+    for trial in range(3):
+        logits = torch.randn((T, E), generator=g)
+        bias = None
+        if where == "logits":
+            at = torch.rand((T, E), generator=g).argsort(1)[:, :4]
+            if trial == 0:   # neighbours
+                at = torch.randint(0, E - 3, (T, 1), generator=g) + torch.arange(4)[None, :]
+            logits.scatter_(1, at, math.inf)
+        else:
+            bias = torch.zeros(E)
+            first = int(torch.randint(0, E - 3, (1,), generator=g))
+            bias[first:first + 4 if trial == 0 else first + 1] = math.inf
+            bias[torch.randperm(E, generator=g)[:4 * (trial > 0)]] = math.inf
+        b = None if bias is None else bias.to(DEV)
+        for k, gtop in ((1, 1), (2, 1), (3, 2 if bias is not None and groups > 1 else 1)):
+            re, _, _ = ref_route(logits[rows], k, bias, "sigmoid", groups, top, gtop)
+            for dtype in (torch.float32, torch.bfloat16):
+                if dtype == torch.bfloat16:
+                    re, _, _ = ref_route(logits[rows].to(dtype), k, bias, "sigmoid", groups, top,
+                                         gtop)
+                x = logits.to(dtype).to(DEV)
+                for view in (x, offset_view(x, 1)):
+                    e, _, _ = sfn.route_experts(view, k, bias=b, score="sigmoid", groups=groups,
+                                                top_groups=top, group_top=gtop)
+                    assert np.array_equal(e.cpu()[rows].numpy(), re), (k, dtype, trial)
+
+
+@pytest.mark.parametrize("E,groups", [(64, 8), (48, 6), (256, 8), (100, 5)])
+def test_route_group_sums_past_the_range(E, groups):
+    """Sums of two scores that pass float32's range (finite biases near its end)
+    are told apart: the larger sum stays, not the lower group."""
+    T, size = 20, E // groups
+    logits = rand(E, T, E)
+    bias = torch.zeros(E)
+    bias[size:size + 2] = 2.9e38
+    bias[3 * size + 1:3 * size + 3] = 3.3e38
+    bias[4 * size:4 * size + 2] = 3.1e38
+    for top in (1, 2):
+        for score in ("softmax", "sigmoid"):
+            e, _, _ = sfn.route_experts(logits.to(DEV), 2, bias=bias.to(DEV), score=score,
+                                        groups=groups, top_groups=top, group_top=2)
+            re, _, _ = ref_route(logits, 2, bias, score, groups, top, 2)
+            assert np.array_equal(e.cpu().numpy(), re)
+            assert (e[:, 0] // size == 3).all()
