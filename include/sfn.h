@@ -329,7 +329,8 @@ sfn_status sfn_sparse_ffn_backward(const void *x, const void *A, const void *B, 
  *   Of the experts that stay, the k of largest c, in descending order, equal
  *       ones to the lower index; NaN ranks below every number.
  *   w_i = scale s_i / (sum over the k of s) if renormalize (0 where that sum
- *       is 0), else scale s_i.
+ *       is 0 in float64: where the chosen logits are more than 745 below the
+ *       row's largest, or with sigmoid scores below -709), else scale s_i.
  * A slot left without an expert (its c is -inf: the token's mask leaves fewer
  * than k) is empty: expert -1, weight 0.  A row of -inf has softmax scores 0.
  * Under softmax a NaN or +inf logit makes every score and weight of its row

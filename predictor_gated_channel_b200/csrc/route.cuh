@@ -113,6 +113,22 @@ __device__ __forceinline__ R score_of(float l, bool sigmoid, float m, R z) {
   return z == R(0) ? R(0) : exp_of((R)l - (R)m) / z;
 }
 
+// A chosen expert's share in the renormalised weights, up to a factor that all of
+// the row's shares have: exp(-m) s with m the row's largest chosen logit `top`
+// (softmax; its sum over the row cancels) or the smaller of it and 0 (sigmoid), so
+// that the shares of scores below float32's range are not lost.  The largest share
+// is at least 1/2.
+__device__ __forceinline__ float share_of(float l, bool sigmoid, float top) {
+  if (!sigmoid) return expf(l - top);
+  const float m = fminf(top, 0.f);
+  return 1.f / (expf(m) + expf(m - l));
+}
+// Are the chosen scores 0, as float64 gives them?  (m: the row's largest logit;
+// softmax only.)  Then the weights are, as masks of a type's lowest value mean it.
+__device__ __forceinline__ bool shares_vanish(bool sigmoid, float top, float m) {
+  return sigmoid ? top < -709.7827f : top == -INFINITY || top - m < -745.1332f;
+}
+
 template <class R>
 __device__ __forceinline__ R select_score(R s, float l, float b) {
   return (l == -INFINITY || b == -INFINITY) ? (R)-INFINITY : s + (R)b;

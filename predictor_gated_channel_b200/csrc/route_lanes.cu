@@ -233,9 +233,10 @@ __global__ void __launch_bounds__(32 * kWarps, (lanes_blocks<V, kByLogit>()))
     if (bp == -INFINITY) lp = -INFINITY;
     const bool empty = lp == -INFINITY;
     float weight;
-    if (p.renorm && !p.sigmoid) {
-      const uint32_t key = lanes_max(empty ? 0u : order_key(lp));
-      weight = empty ? 0.f : expf(lp - key_value(key));
+    if (p.renorm) {  // as in k_route
+      const float most_l = key_value(lanes_max(empty ? 0u : order_key(lp)));
+      const bool none_left = shares_vanish(p.sigmoid, most_l, kByLogit ? most_l : m);
+      weight = empty || none_left ? 0.f : share_of(lp, p.sigmoid, most_l);
     } else {
       weight = empty ? 0.f : score_of<float>(lp, p.sigmoid, m, z);
     }

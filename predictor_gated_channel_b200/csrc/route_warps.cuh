@@ -52,11 +52,11 @@ __global__ void __launch_bounds__(32 * kWarps, route_blocks<V>()) k_route(const 
     if (bp == -INFINITY) lp = -INFINITY;
     const bool empty = lp == -INFINITY;
     float w;
-    if (p.renorm && !p.sigmoid) {
-      // s_i / sum s: the row's sum cancels; the largest chosen logit in its
-      // place, so that nothing underflows
-      const uint32_t key = __reduce_max_sync(kFull, empty ? 0u : order_key(lp));
-      w = empty ? 0.f : expf(lp - key_value(key));
+    if (p.renorm) {
+      const float top = key_value(__reduce_max_sync(kFull, empty ? 0u : order_key(lp)));
+      // (ranked by logits, a softmax row's largest is among the chosen)
+      const bool none = shares_vanish(p.sigmoid, top, kByLogit ? top : m);
+      w = empty || none ? 0.f : share_of(lp, p.sigmoid, top);
     } else {
       w = empty ? 0.f : score_of<float>(lp, p.sigmoid, m, z);
     }

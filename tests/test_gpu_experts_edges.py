@@ -12,7 +12,7 @@ import torch
 import predictor_gated_channel_b200 as sfn
 from predictor_gated_channel_b200 import _capi
 from predictor_gated_channel_b200 import build as sfn_build
-from test_gpu_experts import DEV, expert_weights, rand, ref_route
+from test_gpu_experts import DEV, U, expert_weights, rand, ref_route
 
 pytestmark = pytest.mark.gpu
 
@@ -109,3 +109,48 @@ def test_route_group_sums_past_the_range(E, groups):
             re, _, _ = ref_route(logits, 2, bias, score, groups, top, 2)
             assert np.array_equal(e.cpu().numpy(), re)
             assert (e[:, 0] // size == 3).all()
+
+
+# ------------------------------------------------------------------- weights
+@pytest.mark.parametrize("T,E,k,groups,gtop,bias", [
+    (50, 64, 8, 1, 1, False), (50, 100, 5, 1, 1, True), (50, 256, 8, 8, 2, True),
+    (2100, 64, 8, 1, 1, False), (2100, 250, 3, 1, 1, False), (17000, 64, 4, 1, 1, True),
+])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_route_weights_of_tiny_scores(T, E, k, groups, gtop, bias, dtype):
+    """Sigmoid scores below float32's range still share their weight as the
+    definition says, down to where float64 has them as 0."""
+    logits = rand(E, T, E, scale=2.0) - 95.0   # about the end of the range, and past it
+    logits[1::3] -= 200.0
+    logits[2::7] = -690.0 - logits[2::7].abs() / 50   # not below -709
+    logits[3] = torch.finfo(dtype).min         # a mask of the lowest value
+    logits[4, : E // 2] = -math.inf
+    logits = logits.to(dtype)
+    b = torch.round(rand(3, E) * 20) / 1000 if bias else None
+    rows = torch.cat([torch.arange(40), torch.arange(T - 10, T)])
+    e, w, _ = sfn.route_experts(logits.to(DEV), k, bias=None if b is None else b.to(DEV),
+                                score="sigmoid", groups=groups, top_groups=max(1, groups // 2),
+                                group_top=gtop, scale=1.5)
+    re, rw, _ = ref_route(logits[rows], k, b, "sigmoid", groups, max(1, groups // 2), gtop, True,
+                          1.5)
+    assert np.array_equal(e.cpu()[rows].numpy(), re)
+    assert np.allclose(w.cpu()[rows].double().numpy(), rw, rtol=100 * U, atol=1e-37)
+    assert (w[3] == 0).all() and (w[0].sum() - 1.5).abs() < 1e-5
+
+
+@pytest.mark.parametrize("T", [9, 17000])
+def test_route_weights_far_below_the_largest(T):
+    """Experts that a bias sends a token to, far below the row's largest logit:
+    weights as the softmax's ratios have them at gaps of 90 and 200, and 0 where
+    float64 has the scores as 0 (a mask of the lowest value)."""
+    E, k = 64, 4
+    for gap, zero in ((90.0, False), (200.0, False), (float(torch.finfo(torch.float32).max), True)):
+        logits = rand(T, T, E)
+        logits[:, 20:] -= gap
+        bias = torch.zeros(E)
+        bias[:20] = -math.inf
+        e, w, _ = sfn.route_experts(logits.to(DEV), k, bias=bias.to(DEV))
+        re, rw, _ = ref_route(logits[:9], k, bias)
+        assert np.array_equal(e.cpu()[:9].numpy(), re)
+        assert np.allclose(w.cpu()[:9].double().numpy(), rw, rtol=100 * U, atol=1e-37)
+        assert (w == 0).all() if zero else ((w.sum(1) - 1).abs() < 1e-5).all()
