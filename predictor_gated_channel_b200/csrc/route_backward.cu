@@ -1,9 +1,14 @@
 // route_backward.cu -- the gradient of routing (route.cuh).
 //
-// The gradient: with n_i = s_i / sum_j s_j,
-//   ds_i = scale (dw_i - sum_j dw_j n_j) / sum_j s_j (renormalised), or
-//   ds_i = scale dw_i; plus a dense ds (a balance loss on the scores)
+// Through the scores: with ds a dense gradient of them (a balance loss), plus
+// scale dw_i on the chosen experts where the weights are not renormalised,
 //   softmax: dl = s (ds - sum_e s_e ds_e);  sigmoid: dl = s (1 - s) ds
+// Renormalised weights: with the shares n_i = s_i / sum_j s_j (share_of()) the
+// chosen logits' gradients are, on top of that,
+//   v_i = scale n_i (dw_i - sum_j n_j dw_j), with sigmoid scores times 1 - s_i
+// (with softmax the sum over the row of s ds is 0 for this part).  So formed, it
+// does not depend on how small the chosen scores are in the row: through ds_i =
+// v_i / s_i it would pass float32's range where they are 90 below the largest.
 #include "route.cuh"
 
 namespace sfn {
@@ -63,6 +68,12 @@ __device__ __forceinline__ void store_row(void *out, int64_t t, int E, const flo
   }
 }
 
+// s (1 - s) of a sigmoid score: 1 - sigma(l) = sigma(-l), without the cancellation.
+__device__ __forceinline__ float slope(float l) {
+  const float x = expf(-fabsf(l)), q = 1.f / (1.f + x);
+  return (x * q) * q;
+}
+
 // Blocks of kWarps rows an SM holds at once.
 template <int V>
 constexpr int backward_blocks() {
@@ -71,12 +82,11 @@ constexpr int backward_blocks() {
 
 // One warp per row.
 // kDense: every score of the row is needed (softmax without renormalisation,
-// or a dscores): the slots' ds are added to the lanes' values in slot order,
+// or a dscores): the slots' parts are added to the lanes' values in slot order,
 // and the row is written once.  Otherwise the gradient outside the chosen
-// experts is 0: for the renormalised softmax sum_e s_e ds_e = scale (sum_i dw_i
-// n_i - sum_j dw_j n_j sum_i n_i) / D = 0, and s_i / D needs the chosen logits
-// only; the row is written as zeros and, after a warp barrier that orders the
-// two, the chosen experts' gradients over it, lane i slot i's.
+// experts is 0 and theirs needs their logits only; the row is written as zeros
+// and, after a warp barrier that orders the two, the chosen experts' gradients
+// over it, lane i slot i's.
 template <bool kBf16, int V, bool kBlocked, bool kDense>
 __global__ void __launch_bounds__(32 * kWarps, backward_blocks<V>())
     k_route_bwd(const RouteBwdParams p) {
@@ -114,12 +124,12 @@ __global__ void __launch_bounds__(32 * kWarps, backward_blocks<V>())
       }
     }
     if (t + stride < p.T) fetch(t + stride);
-    float m = 0.f, z = 1.f;
-    if (!p.sigmoid) {
-      if constexpr (kDense) {
+    float m = 0.f;
+    if constexpr (kDense) {
+      if (!p.sigmoid) {
         // l becomes the row's scores
         m = row_max<V>(l);
-        z = 0.f;
+        float z = 0.f;
 #pragma unroll
         for (int j = 0; j < V; ++j) {
           l[j] = m == -INFINITY ? 0.f : expf(l[j] - m);
@@ -129,36 +139,41 @@ __global__ void __launch_bounds__(32 * kWarps, backward_blocks<V>())
         const float inv = z == 0.f ? 0.f : 1.f / z;
 #pragma unroll
         for (int j = 0; j < V; ++j) l[j] *= inv;
-      } else {
-        // only the ratio to the chosen experts' sum matters
-        const uint32_t key = __reduce_max_sync(kFull, e >= 0 ? order_key(le) : 0u);
-        m = key == 0u ? le : key_value(key);
-        if (m == -INFINITY) z = 0.f;
       }
     }
-    float d = p.scale * dw, s = 0.f;
-    if (p.renorm || !kDense) s = e >= 0 ? score_of<float>(le, p.sigmoid, m, z) : 0.f;
+    float d = p.scale * dw;  // the slot's: of its score, or (renormalised) of its logit
     if (p.renorm) {
+      const float top = key_value(__reduce_max_sync(kFull, e >= 0 ? order_key(le) : 0u));
+      const bool none = shares_vanish(p.sigmoid, top, kDense ? m : top);
+      const float part = e < 0 || none ? 0.f : share_of(le, p.sigmoid, top);
       // dw_i - sum_j dw_j n_j on the differences from one slot's dw: the sum of
       // the n is 1, and what all slots have in common (for k = 1 everything)
       // then cancels exactly
       const int ref = __ffs(__ballot_sync(kFull, e >= 0)) - 1;
       const float by = dw - __shfl_sync(kFull, dw, ref < 0 ? 0 : ref);
-      const float sum = warp_add(s);
-      const float mean = sum == 0.f ? 0.f : warp_add(by * s) / sum;
-      d = sum == 0.f ? 0.f : p.scale * (by - mean) / sum;
+      const float sum = warp_add(part), dot = warp_add(by * part);
+      const float inv = sum == 0.f ? 0.f : 1.f / sum;
+      d = p.scale * (part * inv) * (by - dot * inv);
+      if (p.sigmoid) d *= 1.f / (1.f + expf(le));
+    } else if (!kDense) {
+      d *= slope(le);
     }
+    if (e < 0) d = 0.f;
     float g[V];
     if constexpr (kDense) {
-      for (int i = 0; i < p.k; ++i) {
-        const int ei = __shfl_sync(kFull, e, i);
-        const float di = __shfl_sync(kFull, d, i);
-        // the owner lane and the value's place in it (-1: an empty slot, nobody)
-        const int at = ei < 0 ? -1 : (kBlocked ? ei - lane * V : ((ei & 31) == lane ? ei >> 5 : -1));
+      auto to_slots = [&](float (&v)[V]) {  // v += the slots' d
+        for (int i = 0; i < p.k; ++i) {
+          const int ei = __shfl_sync(kFull, e, i);
+          const float di = __shfl_sync(kFull, d, i);
+          // the owner lane and the value's place in it (-1: an empty slot, nobody)
+          const int at =
+              ei < 0 ? -1 : (kBlocked ? ei - lane * V : ((ei & 31) == lane ? ei >> 5 : -1));
 #pragma unroll
-        for (int j = 0; j < V; ++j)
-          if (at == j) ds[j] += di;
-      }
+          for (int j = 0; j < V; ++j)
+            if (at == j) v[j] += di;
+        }
+      };
+      if (!p.renorm) to_slots(ds);
       if (!p.sigmoid) {
         float dot = 0.f;
 #pragma unroll
@@ -171,20 +186,16 @@ __global__ void __launch_bounds__(32 * kWarps, backward_blocks<V>())
 #pragma unroll
         for (int j = 0; j < V; ++j) g[j] = l[j] * (ds[j] - dot);
       } else {
-        // 1 - sigma(l) = sigma(-l), without the cancellation
 #pragma unroll
-        for (int j = 0; j < V; ++j) {
-          const float x = expf(-fabsf(l[j])), q = 1.f / (1.f + x);
-          g[j] = ds[j] * (x * q) * q;
-        }
+        for (int j = 0; j < V; ++j) g[j] = ds[j] * slope(l[j]);
       }
+      if (p.renorm) to_slots(g);
       store_row<kBf16, V, kBlocked>(p.dlogits, t, p.E, g);
     } else {
 #pragma unroll
       for (int j = 0; j < V; ++j) g[j] = 0.f;
       store_row<kBf16, V, kBlocked>(p.dlogits, t, p.E, g);
       // the same expert in two slots: the first of them takes the sum
-      if (e < 0) d = 0.f;
       bool first = e >= 0;
       const uint32_t same = __match_any_sync(kFull, e >= 0 ? e : -1 - lane);
       if (__any_sync(kFull, __popc(same) > 1)) {
@@ -197,14 +208,7 @@ __global__ void __launch_bounds__(32 * kWarps, backward_blocks<V>())
         first = first && __ffs(same) - 1 == lane;
       }
       __syncwarp();
-      if (first) {
-        float ge = s * d;
-        if (p.sigmoid) {
-          const float x = expf(-fabsf(le)), q = 1.f / (1.f + x);
-          ge = d * (x * q) * q;
-        }
-        store_grad<kBf16>(p.dlogits, t * p.E + e, ge);
-      }
+      if (first) store_grad<kBf16>(p.dlogits, t * p.E + e, d);
     }
   }
 }
@@ -245,9 +249,9 @@ __global__ void __launch_bounds__(32 * kWarps, (lanes_blocks<V, false>()))
     for (int j = 0; j < V; ++j)
       // values past E have the score 0; their ds must not be -inf
       if (p.dscores == nullptr || (!kBlocked && sub + kRowLanes * j >= p.E)) ds[j] = 0.f;
-    float s = 0.f;  // the slot's score
+    float s = 0.f, m = 0.f;  // the slot's score; the row's largest logit
     if (!p.sigmoid) {
-      float m = l[0];
+      m = l[0];
 #pragma unroll
       for (int j = 1; j < V; ++j) m = fmaxf(m, l[j]);
       const uint32_t key = lanes_max(order_key(m));
@@ -263,21 +267,22 @@ __global__ void __launch_bounds__(32 * kWarps, (lanes_blocks<V, false>()))
 #pragma unroll
       for (int j = 0; j < V; ++j) l[j] *= inv;
       if (e >= 0 && m != -INFINITY) s = expf(le - m) * inv;
-    } else if (e >= 0) {
-      s = score_of<float>(le, true, 0.f, 1.f);
     }
     float d = p.scale * dw;
     if (p.renorm) {
-      const float sum = lanes_add(s);
-      // as in k_route_bwd; by all lanes: the rows of a warp differ in sum
+      // as in k_route_bwd; collectives by all lanes: the rows of a warp differ
+      const float top = key_value(lanes_max(e >= 0 ? order_key(le) : 0u));
+      const bool none = shares_vanish(p.sigmoid, top, m);
+      const float part = e < 0 || none ? 0.f : share_of(le, p.sigmoid, top);
       const uint32_t used = __ballot_sync(kFull, e >= 0) & (0xffu << first);
       const float by = dw - __shfl_sync(kFull, dw, used == 0u ? first : __ffs(used) - 1);
-      const float dot = lanes_add(by * s);
-      const float mean = sum == 0.f ? 0.f : dot / sum;
-      d = sum == 0.f ? 0.f : p.scale * (by - mean) / sum;
+      const float sum = lanes_add(part), dot = lanes_add(by * part);
+      const float inv = sum == 0.f ? 0.f : 1.f / sum;
+      d = p.scale * (part * inv) * (by - dot * inv);
+      if (p.sigmoid) d *= 1.f / (1.f + expf(le));
     }
     if (e < 0) d = 0.f;
-    const float mine = s * d;  // of the row's sum of s ds
+    const float mine = p.renorm ? 0.f : s * d;  // of the row's sum of s ds
     // the same expert in two slots: the first of them takes the sum
     bool store = e >= 0;
     const uint32_t same = __match_any_sync(kFull, e >= 0 ? first / kRowLanes * p.E + e : -1 - lane);
@@ -298,16 +303,11 @@ __global__ void __launch_bounds__(32 * kWarps, (lanes_blocks<V, false>()))
       dot = lanes_add(dot);
 #pragma unroll
       for (int j = 0; j < V; ++j) g[j] = l[j] * (ds[j] - dot);
-      ge = s * (de + d - dot);
+      ge = p.renorm ? s * (de - dot) + d : s * (de + d - dot);
     } else {
-      // 1 - sigma(l) = sigma(-l), without the cancellation
-      auto slope = [](float x) {
-        const float y = expf(-fabsf(x)), q = 1.f / (1.f + y);
-        return (y * q) * q;
-      };
 #pragma unroll
       for (int j = 0; j < V; ++j) g[j] = ds[j] * slope(l[j]);
-      ge = (de + d) * slope(le);
+      ge = p.renorm ? de * slope(le) + d : (de + d) * slope(le);
     }
     if (live) store_row<kBf16, V, kBlocked, kRowLanes>(p.dlogits, t, p.E, g);
     __syncwarp();

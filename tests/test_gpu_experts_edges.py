@@ -12,7 +12,7 @@ import torch
 import predictor_gated_channel_b200 as sfn
 from predictor_gated_channel_b200 import _capi
 from predictor_gated_channel_b200 import build as sfn_build
-from test_gpu_experts import DEV, U, expert_weights, rand, ref_route
+from test_gpu_experts import BF16, DEV, U, expert_weights, rand, ref_route
 
 pytestmark = pytest.mark.gpu
 
@@ -154,3 +154,60 @@ def test_route_weights_far_below_the_largest(T):
         assert np.array_equal(e.cpu()[:9].numpy(), re)
         assert np.allclose(w.cpu()[:9].double().numpy(), rw, rtol=100 * U, atol=1e-37)
         assert (w == 0).all() if zero else ((w.sum(1) - 1).abs() < 1e-5).all()
+
+
+# ------------------------------------------------------------------ gradients
+def parts_of_gradient(logits, experts, dw, score):
+    """In 64 bits: the row's scores, the chosen experts' shares n and v, the gradient of
+    the chosen logits through the renormalised weights."""
+    l = logits.double()
+    s = torch.softmax(l, 1) if score == "softmax" else torch.sigmoid(l)
+    at, there = experts.long().clamp(min=0), experts >= 0
+    n = s.gather(1, at) * there
+    total = n.sum(1, keepdim=True)
+    n = n / torch.where(total > 0, total, torch.ones_like(total))
+    v = n * (dw.double() - (n * dw.double()).sum(1, keepdim=True))
+    if score == "sigmoid":
+        v = v * torch.sigmoid(-l).gather(1, at)
+    return s, n, v, at
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("dense", ["none", "zeros", "random"])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("T", [50, 9000])
+def test_route_backward_of_tiny_scores(T, score, dense, dtype):
+    """Chosen logits far below an unchosen one (softmax; a bias or a group choice
+    does that) or far down the sigmoid: the gradient of the renormalised weights
+    depends on the chosen logits alone, and is finite.
+
+    v is right to 322 u n max |dw| scale: a share to 40 u, the differences from one
+    slot's dw (at most 2 max |dw|) to u, their mean to 80 u."""
+    E, k = 64, 6
+    gaps = torch.tensor([60.0, 88.0, 90.0, 100.0, 104.0, 120.0, 300.0])
+    logits = rand(T, T, E)
+    experts = torch.stack([torch.randperm(E - 1, generator=torch.Generator().manual_seed(t))[:k]
+                           for t in range(200)]).repeat(T // 200 + 1, 1)[:T]
+    low = -gaps[torch.arange(T) % len(gaps)][:, None]
+    logits = logits.scatter(1, experts, (logits + low).gather(1, experts)).to(dtype)
+    experts = experts.to(torch.int32)
+    experts[::5, 2] = -1
+    dw = rand(7, T, k)
+    ds = None if dense == "none" else rand(8, T, E) * (dense == "random")
+    got = sfn.route_experts_backward(logits.to(DEV), experts.to(DEV), dw.to(DEV), scale=1.5,
+                                     dscores=None if ds is None else ds.to(DEV), score=score)
+    s, n, v, at = parts_of_gradient(logits, experts, dw, score)
+    big = dw.double().abs().amax(1, keepdim=True)
+    ref = torch.zeros_like(s).scatter_add(1, at, 1.5 * v * (experts >= 0))
+    tol = torch.zeros_like(s).scatter_add(1, at, 1.5 * 322 * U * n * big)
+    if ds is not None:
+        d = ds.double()
+        if score == "softmax":
+            ref += s * (d - (s * d).sum(1, keepdim=True))
+        else:
+            ref += s * torch.sigmoid(-logits.double()) * d
+        tol += 200 * U * s * d.abs().amax(1, keepdim=True)
+    tol += 1e-37
+    if dtype == torch.bfloat16:
+        tol += BF16 * ref.abs()
+    assert ((got.cpu().double() - ref).abs() <= tol).all()
