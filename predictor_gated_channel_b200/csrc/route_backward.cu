@@ -143,13 +143,17 @@ __global__ void __launch_bounds__(32 * kWarps, backward_blocks<V>())
     }
     float d = p.scale * dw;  // the slot's: of its score, or (renormalised) of its logit
     if (p.renorm) {
-      const float top = key_value(__reduce_max_sync(kFull, e >= 0 ? order_key(le) : 0u));
+      const uint32_t key = e >= 0 ? order_key(le) : 0u;
+      const uint32_t top_key = __reduce_max_sync(kFull, key);
+      const float top = key_value(top_key);
       const bool none = shares_vanish(p.sigmoid, top, kDense ? m : top);
       const float part = e < 0 || none ? 0.f : share_of(le, p.sigmoid, top);
       // dw_i - sum_j dw_j n_j on the differences from one slot's dw: the sum of
       // the n is 1, and what all slots have in common (for k = 1 everything)
-      // then cancels exactly
-      const int ref = __ffs(__ballot_sync(kFull, e >= 0)) - 1;
+      // then cancels exactly.  The slot of the largest score (its n is at least
+      // 1 / k), so that a large dw of a slot with next to no weight stays out of
+      // the others' gradients.
+      const int ref = __ffs(__ballot_sync(kFull, e >= 0 && key == top_key)) - 1;
       const float by = dw - __shfl_sync(kFull, dw, ref < 0 ? 0 : ref);
       const float sum = warp_add(part), dot = warp_add(by * part);
       const float inv = sum == 0.f ? 0.f : 1.f / sum;
@@ -271,11 +275,13 @@ __global__ void __launch_bounds__(32 * kWarps, (lanes_blocks<V, false>()))
     float d = p.scale * dw;
     if (p.renorm) {
       // as in k_route_bwd; collectives by all lanes: the rows of a warp differ
-      const float top = key_value(lanes_max(e >= 0 ? order_key(le) : 0u));
+      const uint32_t key = e >= 0 ? order_key(le) : 0u;
+      const uint32_t top_key = lanes_max(key);
+      const float top = key_value(top_key);
       const bool none = shares_vanish(p.sigmoid, top, m);
       const float part = e < 0 || none ? 0.f : share_of(le, p.sigmoid, top);
-      const uint32_t used = __ballot_sync(kFull, e >= 0) & (0xffu << first);
-      const float by = dw - __shfl_sync(kFull, dw, used == 0u ? first : __ffs(used) - 1);
+      const uint32_t at_top = __ballot_sync(kFull, e >= 0 && key == top_key) & (0xffu << first);
+      const float by = dw - __shfl_sync(kFull, dw, at_top == 0u ? first : __ffs(at_top) - 1);
       const float sum = lanes_add(part), dot = lanes_add(by * part);
       const float inv = sum == 0.f ? 0.f : 1.f / sum;
       d = p.scale * (part * inv) * (by - dot * inv);

@@ -211,3 +211,37 @@ def test_route_backward_of_tiny_scores(T, score, dense, dtype):
     if dtype == torch.bfloat16:
         tol += BF16 * ref.abs()
     assert ((got.cpu().double() - ref).abs() <= tol).all()
+
+
+@pytest.mark.parametrize("dense", [False, True])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("T", [60, 9000])
+def test_route_backward_large_weight_gradient_of_a_small_score(T, score, dense):
+    """One slot (the first, as biases can have it) with a large dweights and next
+    to no weight must not cost the others their precision.
+
+    A share n is right to 40 u (the exponential 4 u, its argument up to 25 u, sum
+    and quotient 10 u), the differences from the largest score's dw (of which n is
+    at least 1 / k: it is at most k M, M = sum n |dw|) to u each, and their mean to
+    80 u of sum n |by| <= (k + 1) M: below 1000 u n_i (|dw_i| + M) in all."""
+    E, k = 96, 8
+    logits = rand(T, T, E, scale=0.5)
+    experts = torch.stack([torch.randperm(E, generator=torch.Generator().manual_seed(t))[:k]
+                           for t in range(200)]).repeat(T // 200 + 1, 1)[:T]
+    logits.scatter_(1, experts[:, :1], -20.0)
+    dw = rand(7, T, k)
+    dw[:, 0] = 1e6
+    ds = torch.zeros((T, E)) if dense else None
+    got = sfn.route_experts_backward(logits.to(DEV), experts.to(torch.int32).to(DEV), dw.to(DEV),
+                                     dscores=None if ds is None else ds.to(DEV), score=score)
+    l = logits.double()
+    s = torch.softmax(l, 1) if score == "softmax" else torch.sigmoid(l)
+    n = s.gather(1, experts)
+    n = n / n.sum(1, keepdim=True)
+    mean_abs = (n * dw.double().abs()).sum(1, keepdim=True)
+    v = n * (dw.double() - (n * dw.double()).sum(1, keepdim=True))
+    if score == "sigmoid":
+        v = v * (1 - s.gather(1, experts))
+    ref = torch.zeros_like(l).scatter(1, experts, v)
+    tol = torch.zeros_like(l).scatter(1, experts, 1000 * U * n * (dw.double().abs() + mean_abs))
+    assert ((got.cpu().double() - ref).abs() <= tol).all()
