@@ -358,8 +358,9 @@ sfn_status sfn_route_experts(const void *logits, sfn_dtype dtype, const float *b
  * loss on the scores), both float32.  The choice itself, and with it the bias,
  * has no gradient.  logits and experts are the forward's; -1 marks an empty
  * slot, whose dweights is not used, and an expert that is in two slots gets the
- * sum of both.  An index outside [-1, E) is taken as empty.  Sums in float32,
- * one rounding at the end.
+ * sum of both.  An index outside [-1, E) is taken as empty.  A softmax row with
+ * a NaN or +inf logit, whose scores and weights are NaN, has gradients NaN, with
+ * and without dscores.  Sums in float32, one rounding at the end.
  */
 sfn_status sfn_route_experts_backward(const void *logits, sfn_dtype dtype,
                                       const int32_t *experts, const float *dweights,

@@ -80,22 +80,29 @@ constexpr int backward_blocks() {
   return V <= 4 ? 10 : (V <= 8 ? 6 : (V <= 16 ? 4 : 2));
 }
 
+// What of a row's logits the gradient needs.
+// kDense: every score (softmax without renormalisation, or a dscores): the
+// slots' parts are added to the lanes' values in slot order, and the row is
+// written once.  Otherwise the gradient outside the chosen experts is 0 and
+// theirs needs their shares only; the row is written as zeros and, after a warp
+// barrier that orders the two, the chosen experts' gradients over it, lane i slot
+// i's.
+// kRow (softmax): the largest, and whether one is NaN or +inf: then the row's
+// scores, weights and gradients are NaN.
+// kChosen (sigmoid): the chosen ones.
+enum class Needs { kChosen, kRow, kDense };
+
 // One warp per row.
-// kDense: every score of the row is needed (softmax without renormalisation,
-// or a dscores): the slots' parts are added to the lanes' values in slot order,
-// and the row is written once.  Otherwise the gradient outside the chosen
-// experts is 0 and theirs needs their logits only; the row is written as zeros
-// and, after a warp barrier that orders the two, the chosen experts' gradients
-// over it, lane i slot i's.
-template <bool kBf16, int V, bool kBlocked, bool kDense>
+template <bool kBf16, int V, bool kBlocked, Needs kNeeds>
 __global__ void __launch_bounds__(32 * kWarps, backward_blocks<V>())
     k_route_bwd(const RouteBwdParams p) {
   pdl_wait();
   pdl_launch_dependents();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t stride = (int64_t)gridDim.x * kWarps;
+  constexpr bool kDense = kNeeds == Needs::kDense, kLogits = kNeeds != Needs::kChosen;
   // the next row's inputs are on their way while this one is done
-  constexpr int kRow = kDense ? V : 1;
+  constexpr int kRow = kLogits ? V : 1;
   int next_e = -1;
   float next_dw = 0.f, next_l[kRow], next_ds[kRow];
   auto fetch = [&](int64_t t) {
@@ -103,10 +110,9 @@ __global__ void __launch_bounds__(32 * kWarps, backward_blocks<V>())
       next_e = p.experts[t * p.k + lane];
       next_dw = p.dweights[t * p.k + lane];
     }
-    if constexpr (kDense) {
-      load_row<kBf16, V, kBlocked>(p.logits, t, p.E, next_l);
+    if constexpr (kLogits) load_row<kBf16, V, kBlocked>(p.logits, t, p.E, next_l);
+    if constexpr (kDense)
       if (p.dscores != nullptr) load_row<false, V, kBlocked>(p.dscores, t, p.E, next_ds);
-    }
   };
   int64_t t = (int64_t)blockIdx.x * kWarps + warp;
   if (t < p.T) fetch(t);
@@ -116,15 +122,23 @@ __global__ void __launch_bounds__(32 * kWarps, backward_blocks<V>())
     const float dw = e >= 0 ? next_dw : 0.f;  // an empty slot's says nothing
     float le = -INFINITY, l[kRow], ds[kRow];
     if (e >= 0) le = load_logit<kBf16>(p.logits, t * p.E + e);
+    if constexpr (kLogits) {
+#pragma unroll
+      for (int j = 0; j < V; ++j) l[j] = next_l[j];
+    }
     if constexpr (kDense) {
 #pragma unroll
-      for (int j = 0; j < V; ++j) {
-        l[j] = next_l[j];
-        ds[j] = p.dscores != nullptr ? next_ds[j] : 0.f;
-      }
+      for (int j = 0; j < V; ++j) ds[j] = p.dscores != nullptr ? next_ds[j] : 0.f;
     }
     if (t + stride < p.T) fetch(t + stride);
     float m = 0.f;
+    bool bad = false;
+    if constexpr (kLogits && !kDense) {
+      m = row_max<V>(l);
+#pragma unroll
+      for (int j = 0; j < V; ++j) bad |= !(l[j] < INFINITY);
+      bad = __any_sync(kFull, bad);
+    }
     if constexpr (kDense) {
       if (!p.sigmoid) {
         // l becomes the row's scores
@@ -146,7 +160,7 @@ __global__ void __launch_bounds__(32 * kWarps, backward_blocks<V>())
       const uint32_t key = e >= 0 ? order_key(le) : 0u;
       const uint32_t top_key = __reduce_max_sync(kFull, key);
       const float top = key_value(top_key);
-      const bool none = shares_vanish(p.sigmoid, top, kDense ? m : top);
+      const bool none = shares_vanish(p.sigmoid, top, kLogits ? m : top);
       const float part = e < 0 || none ? 0.f : share_of(le, p.sigmoid, top);
       // dw_i - sum_j dw_j n_j on the differences from one slot's dw: the sum of
       // the n is 1, and what all slots have in common (for k = 1 everything)
@@ -197,7 +211,7 @@ __global__ void __launch_bounds__(32 * kWarps, backward_blocks<V>())
       store_row<kBf16, V, kBlocked>(p.dlogits, t, p.E, g);
     } else {
 #pragma unroll
-      for (int j = 0; j < V; ++j) g[j] = 0.f;
+      for (int j = 0; j < V; ++j) g[j] = bad ? __int_as_float(0x7fc00000) : 0.f;
       store_row<kBf16, V, kBlocked>(p.dlogits, t, p.E, g);
       // the same expert in two slots: the first of them takes the sum
       bool first = e >= 0;
@@ -212,7 +226,7 @@ __global__ void __launch_bounds__(32 * kWarps, backward_blocks<V>())
         first = first && __ffs(same) - 1 == lane;
       }
       __syncwarp();
-      if (first) store_grad<kBf16>(p.dlogits, t * p.E + e, d);
+      if (first && !bad) store_grad<kBf16>(p.dlogits, t * p.E + e, d);
     }
   }
 }
@@ -353,15 +367,17 @@ cudaError_t launch_route_backward(const RouteShape &s, const void *logits,
   return with_layout(s.E, vectors, false, [&](auto v, auto blocked) {
     constexpr int V = decltype(v)::value;
     constexpr bool kB = decltype(blocked)::value;
-    auto go = [&](auto bf16, auto all) {
+    auto go = [&](auto bf16, auto needs) {
       if constexpr (kB && !vector_part<V>())  // (not reached, and not built)
         return cudaErrorInvalidValue;
       else
-        return launch_rows(k_route_bwd<decltype(bf16)::value, V, kB, decltype(all)::value>, s.T,
+        return launch_rows(k_route_bwd<decltype(bf16)::value, V, kB, decltype(needs)::value>, s.T,
                            backward_blocks<V>(), 0, num_sms, st, p);
     };
     auto with_all = [&](auto bf16) {
-      return dense ? go(bf16, std::true_type{}) : go(bf16, std::false_type{});
+      if (dense) return go(bf16, std::integral_constant<Needs, Needs::kDense>{});
+      return s.sigmoid ? go(bf16, std::integral_constant<Needs, Needs::kChosen>{})
+                       : go(bf16, std::integral_constant<Needs, Needs::kRow>{});
     };
     return s.bf16 ? with_all(std::true_type{}) : with_all(std::false_type{});
   });

@@ -245,3 +245,26 @@ def test_route_backward_large_weight_gradient_of_a_small_score(T, score, dense):
     ref = torch.zeros_like(l).scatter(1, experts, v)
     tol = torch.zeros_like(l).scatter(1, experts, 1000 * U * n * (dw.double().abs() + mean_abs))
     assert ((got.cpu().double() - ref).abs() <= tol).all()
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("dense", [False, True])
+@pytest.mark.parametrize("T,E", [(50, 64), (50, 33), (50, 1000), (9000, 100), (9000, 256)])
+def test_route_backward_of_rows_that_are_no_numbers(T, E, dense, dtype):
+    """A NaN or +inf logit makes its softmax row's scores and weights NaN, and so
+    its gradients, chosen or not; the other rows are what they are without it."""
+    k = 4
+    logits = rand(T, T, E).to(dtype)
+    experts = torch.topk(logits[:, : E - 1].float(), k, dim=1).indices.to(torch.int32)
+    dw = rand(7, T, k).to(DEV)
+    ds = torch.zeros((T, E), device=DEV) if dense else None
+    clean = sfn.route_experts_backward(logits.to(DEV), experts.to(DEV), dw, dscores=ds)
+    bad = {3: (E - 1, math.nan), 7: (E - 1, math.inf), 11: (int(experts[11, 0]), math.nan),
+           T - 1: (int(experts[T - 1, 1]), math.inf)}
+    for t, (e, value) in bad.items():
+        logits[t, e] = value
+    got = sfn.route_experts_backward(logits.to(DEV), experts.to(DEV), dw, dscores=ds)
+    rows = torch.zeros(T, dtype=torch.bool, device=DEV)
+    rows[list(bad)] = True
+    assert torch.isnan(got[rows]).all()
+    assert torch.equal(got[~rows], clean[~rows])
