@@ -337,8 +337,9 @@ sfn_status sfn_sparse_ffn_backward(const void *x, const void *A, const void *B, 
  * NaN.
  *
  * The choice does not depend on rounding: without a bias experts are ranked
- * by their logits, else by c as float64 gives it, so the same logits choose
- * the same experts in every call, whatever the batch around them.
+ * by their logits, and groups by their largest one (group_top 1); sums of two
+ * scores, and everything with a bias, by c as float64 gives it.  The same
+ * logits choose the same experts in every call, whatever the batch around them.
  *
  * logits [T][E] in `dtype`; experts int32 [T][k]; weights float32 [T][k];
  * scores (may be NULL) receives s, float32 [T][E].  1 <= k <= 32, E <= 1024,

@@ -12,10 +12,10 @@
 // A slot whose c is -inf is empty: expert -1, weight 0.
 //
 // The choice does not depend on rounding.  Without a bias the ranking of c is
-// the ranking of l and is done on l itself.  With one, c is computed in
-// float32 and every decision the row took (between neighbours in the order,
-// at the k-th place, between groups) is checked against a bound on the error
-// of c; what is inside the bound is decided again in float64.
+// the ranking of l and is done on l itself (groups by their two largest: on c).
+// With one, c is computed in float32 and every decision the row took (between
+// neighbours in the order, at the k-th place, between groups) is checked against
+// a bound on the error of c; what is inside the bound is decided again in float64.
 //
 // One warp per row, V = E / 32 (rounded up to a built one) values a lane.
 // What bounds it is instruction issue, so the picks run on packed keys: the
@@ -142,12 +142,14 @@ __device__ __forceinline__ int expert_of(int j) {
 }
 
 // The k experts of one row, from the selection scores c of this lane's
-// experts (those past E are never looked at).  Lane i returns slot i's
+// experts (those past E are never looked at): groups by c, the experts of those
+// that stay by c too or, by_l, by their logits l.  Lane i returns slot i's
 // expert.  `next`: the best expert left over (kNone: none).  gap_lo and
 // gap_hi: the worst score of a kept group and the best of a dropped one.
 template <int V, bool kBlocked, class R>
-__device__ __noinline__ int choose(const R (&c)[V], const RouteParams &p, R *row_smem, int &next,
-                                   R &gap_lo, R &gap_hi) {
+__device__ __noinline__ int choose(const R (&c)[V], const float (&l)[V], bool by_l,
+                                   const RouteParams &p, R *row_smem, int &next, R &gap_lo,
+                                   R &gap_hi) {
   using Key = decltype(key_of(R(0)));
   const int lane = threadIdx.x & 31;
   uint32_t gone = 0u;  // bit j: value j is out
@@ -219,7 +221,7 @@ __device__ __noinline__ int choose(const R (&c)[V], const RouteParams &p, R *row
   }
   Key key[V];
 #pragma unroll
-  for (int j = 0; j < V; ++j) key[j] = key_of(c[j]);
+  for (int j = 0; j < V; ++j) key[j] = key_of(by_l ? (R)l[j] : c[j]);
   int mine = -1;
   Key bk = 0;
   int bi = kNone;
@@ -442,8 +444,9 @@ __device__ __noinline__ int settle_row(const RouteParams &p, int64_t t, double *
   int next;
   float lo, hi;
   if constexpr (kByLogit) {
-    return choose<V, false, float>(l, p, row32, next, lo, hi);
+    return choose<V, false, float>(l, l, true, p, row32, next, lo, hi);
   } else {
+    const bool by_l = p.bias == nullptr;
     float bias[V];
     bool nan = false;
 #pragma unroll
@@ -463,7 +466,7 @@ __device__ __noinline__ int settle_row(const RouteParams &p, int64_t t, double *
 #pragma unroll
       for (int j = 0; j < V; ++j)
         c[j] = select_score(score_fast(l[j], p.sigmoid, m, z), l[j], bias[j]);
-      const int pick = choose<V, false, float>(c, p, row32, next, lo, hi);
+      const int pick = choose<V, false, float>(c, l, by_l, p, row32, next, lo, hi);
       // Is every decision outside the error of c?  Lane i < k compares slot i
       // with slot i + 1, the last slot with the best left over.
       auto score_at = [&](int e, float &le, float &be, float &se, float &ce) {
@@ -487,10 +490,10 @@ __device__ __noinline__ int settle_row(const RouteParams &p, int64_t t, double *
       if (lane == p.k - 1) score_at(next, l1, b1, s1, c1);
       // equal logits with equal biases are in the right order already
       const bool tie = l0 == l1 && b0 == b1;
-      bool unsure = lane < p.k && c0 > -INFINITY && c1 > -INFINITY && !tie &&
+      bool unsure = !by_l && lane < p.k && c0 > -INFINITY && c1 > -INFINITY && !tie &&
                     !(c0 - c1 > score_error(s0, c0, p.sigmoid) + score_error(s1, c1, p.sigmoid));
       // at the end of the order a third value could hide behind a tie
-      if (lane == p.k - 1 && tie && c1 > -INFINITY) unsure = true;
+      if (!by_l && lane == p.k - 1 && tie && c1 > -INFINITY) unsure = true;
       if (lo > -INFINITY && hi > -INFINITY) {
         // a group's score sums at most two, each at most the largest score
         const float s = p.sigmoid ? 1.f : (z > 0.f ? __fdividef(1.f, z) : 0.f);
@@ -515,7 +518,7 @@ __device__ __noinline__ int settle_row(const RouteParams &p, int64_t t, double *
 #pragma unroll
     for (int j = 0; j < V; ++j)
       c64[j] = select_score(score_of<double>(l[j], p.sigmoid, m, z64), l[j], bias[j]);
-    return choose<V, false, double>(c64, p, row64, next, lo64, hi64);
+    return choose<V, false, double>(c64, l, by_l, p, row64, next, lo64, hi64);
   }
 }
 
@@ -622,7 +625,9 @@ __device__ __noinline__ void exchange_sort(int n, int sub, int first, R &c, int 
 // i's, with its logit and bias.  m, z: the softmax's maximum and sum (kByLogit:
 // not used).  row64: E doubles of shared memory for this warp (kGroups).
 // kByLogit: no bias, and groups (if any) scored by their largest: the logits
-// themselves are ranked.  kGroups: groups > 1.
+// themselves are ranked.  Else, without a bias (groups scored by their two
+// largest), the groups are ranked by scores and their experts by logits.  kGroups:
+// groups > 1.
 template <bool kBf16, int V, bool kBlocked, bool kByLogit, bool kGroups>
 __device__ __forceinline__ int select_row(const RouteParams &p, int64_t t, const float (&l)[V],
                                           const float (&bias)[kByLogit ? 1 : V], bool nan, float m,
@@ -705,6 +710,12 @@ __device__ __forceinline__ int select_row(const RouteParams &p, int64_t t, const
         }
       }
     }
+    // what ranks the experts of the groups that stay
+    const bool by_l = kGroups && !kByLogit && p.bias == nullptr;
+    if (by_l) {
+#pragma unroll
+      for (int j = 0; j < V; ++j) c[j] = l[j];
+    }
     uint32_t w[V];
 #pragma unroll
     for (int j = 0; j < V; ++j) {
@@ -732,7 +743,8 @@ __device__ __forceinline__ int select_row(const RouteParams &p, int64_t t, const
       look_up();
       float cp = -INFINITY;  // the slot's selection score in full
       if (slot)
-        cp = kByLogit ? lp : select_score(score_fast(lp, p.sigmoid, m, z_fast), lp, bp);
+        cp = kByLogit || by_l ? lp
+                              : select_score(score_fast(lp, p.sigmoid, m, z_fast), lp, bp);
       // neighbours whose words agree may be in the wrong order: exchange
       // them, by whole scores and then by index
       float c1 = __shfl_down_sync(kFull, cp, 1);
@@ -747,7 +759,7 @@ __device__ __forceinline__ int select_row(const RouteParams &p, int64_t t, const
       if constexpr (kByLogit) {
         unsure |= lane == p.k - 1 && rest && !(cp > key_value(left | low));
       } else {
-        auto bound = [&](float c) { return score_error(most, c, p.sigmoid); };
+        auto bound = [&](float c) { return by_l ? 0.f : score_error(most, c, p.sigmoid); };
         const float l1 = __shfl_down_sync(kFull, lp, 1), b1 = __shfl_down_sync(kFull, bp, 1);
         bool close = false;
         if (slot && cp > -INFINITY) {
@@ -773,17 +785,19 @@ __device__ __forceinline__ int select_row(const RouteParams &p, int64_t t, const
             lp = load_logit<kBf16>(p.logits, t * p.E + pick);
             if (p.bias != nullptr) bp = __ldg(p.bias + pick);
           }
-          const double z64 = p.sigmoid ? 1.0 : row_sum64<kBf16>(p.logits, t, p.E, m);
+          const double z64 =
+              p.sigmoid || by_l ? 1.0 : row_sum64<kBf16>(p.logits, t, p.E, m);
           double c64 = -INFINITY;
           if (slot || more)
-            c64 = select_score(score_of<double>(lp, p.sigmoid, m, z64), lp, bp);
+            c64 = by_l ? (double)lp
+                       : select_score(score_of<double>(lp, p.sigmoid, m, z64), lp, bp);
           const double c64_1 = __shfl_down_sync(kFull, c64, 1);
           const int e64_1 = __shfl_down_sync(kFull, pick, 1);
           if (__any_sync(kFull, lane < kx - 1 && before(c64_1, e64_1, c64, pick)))
             exchange_sort(kx, lane, 0, c64, pick, lp, bp);
           const double last = __shfl_sync(kFull, c64, p.k - 1);
           const float hi = key_value(left | low);
-          unsure = rest && !((float)last - hi > bound(hi) + 2.f * kUlp * fabsf(hi));
+          unsure = rest && !((float)last - hi > bound(hi) + (by_l ? 0.f : 2.f * kUlp * fabsf(hi)));
         }
       }
     }

@@ -12,7 +12,7 @@ import torch
 import predictor_gated_channel_b200 as sfn
 from predictor_gated_channel_b200 import _capi
 from predictor_gated_channel_b200 import build as sfn_build
-from test_gpu_experts import BF16, DEV, U, expert_weights, rand, ref_route
+from test_gpu_experts import BF16, DEV, U, expert_weights, rand, ref_route, ref_scores
 
 pytestmark = pytest.mark.gpu
 
@@ -268,3 +268,49 @@ def test_route_backward_of_rows_that_are_no_numbers(T, E, dense, dtype):
     rows[list(bad)] = True
     assert torch.isnan(got[rows]).all()
     assert torch.equal(got[~rows], clean[~rows])
+
+
+def choose_by_logits(logits, k, score, groups, top):
+    """No bias, groups by the sum of their two largest scores (float64, ties to the
+    lower group), the experts of those that stay by their logits."""
+    l, s = logits.double().numpy(), ref_scores(logits, score)
+    T, E = l.shape
+    size = E // groups
+    out = np.full((T, k), -1, dtype=np.int32)
+    for t in range(T):
+        marks = []
+        for g in range(groups):
+            best = sorted((s[t, e] for e in range(g * size, (g + 1) * size) if l[t, e] > -np.inf),
+                          reverse=True)[:2]
+            marks.append(sum(best) if best else -np.inf)
+        keep = sorted(range(groups), key=lambda g: (-marks[g], g))[:top]
+        order = sorted((e for e in range(E) if e // size in keep and l[t, e] > -np.inf),
+                       key=lambda e: (-l[t, e], e))[:k]
+        out[t, :len(order)] = order
+    return out
+
+
+@pytest.mark.parametrize("T,E,k,groups,top", [(60, 64, 8, 8, 3), (60, 256, 8, 8, 4),
+                                              (60, 160, 6, 8, 4), (60, 48, 4, 6, 3),
+                                              (60, 100, 5, 5, 2), (60, 384, 31, 16, 9),
+                                              (3000, 64, 8, 4, 2)])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_route_by_logits_within_summed_groups(T, E, k, groups, top, score, dtype):
+    """Without a bias experts are ranked by their logits whatever scores the groups:
+    where float64 has the scores as equal (1 far up the sigmoid, 0 far below a
+    softmax row's largest), where they tie, and where nothing is special."""
+    g = torch.Generator().manual_seed(E)
+    logits = torch.randn((T, E), generator=g) * 1.5
+    whole = torch.round(logits * 4)
+    logits[::3] = whole[::3] + 45.0                        # sigmoid: all 1
+    logits[1::6] = whole[1::6] - 800.0                     # sigmoid: all 0
+    logits[1::6, ::7] = 0.0                                # softmax: 0 but for these
+    logits[2::9] = whole[2::9] / 8
+    logits[5, E // groups + 1:] = -math.inf
+    logits = logits.to(dtype)
+    e, _, _ = sfn.route_experts(logits.to(DEV), k, score=score, groups=groups, top_groups=top,
+                                group_top=2)
+    rows = torch.cat([torch.arange(60), torch.arange(T - 30, T)])
+    assert np.array_equal(e.cpu()[rows].numpy(),
+                          choose_by_logits(logits[rows], k, score, groups, top))
