@@ -383,10 +383,10 @@ sfn_status sfn_quantize_rows_i8(const void *x, sfn_dtype dtype, int8_t *q, float
  * Product in 8-bit integers with a scale for each token and output channel:
  *   y[t][n] = x_scale[t] w_scale[n] sum_k xq[t][k] wq[n][k]
  * with the sum exact in 32 bits; xq [T][K], wq [N][K] (an nn.Linear weight,
- * quantised by sfn_quantize_rows_i8), y [T][N] in y_dtype.  Any T and N, K a
- * multiple of 16 (else SFN_ERR_MISALIGNED) up to 131072 (else
- * SFN_ERR_UNSUPPORTED), the length at which 127^2 K still fits 32 bits; values
- * of -128 are allowed up to K = 131056.
+ * quantised by sfn_quantize_rows_i8), y [T][N] in y_dtype.  K a multiple of 16
+ * (else SFN_ERR_MISALIGNED) up to 131072, the length at which 127^2 K still fits
+ * 32 bits; values of -128 are allowed up to K = 131056.  N up to 2^24, T and the
+ * tiles of 16 rows x 128 channels up to 2^31 - 8193 (else SFN_ERR_UNSUPPORTED).
  */
 sfn_status sfn_matmul_i8(const int8_t *xq, const float *x_scale, const int8_t *wq,
                          const float *w_scale, void *y, sfn_dtype y_dtype, int64_t T, int N,
@@ -415,8 +415,9 @@ sfn_status sfn_linear_i8(const void *x, sfn_dtype x_dtype, const int8_t *wq,
  * error word).  Wg, Wu int8 [E][f][d] with scales float32 [E][f]; Wd int8
  * [E][d][f] with scales [E][d]: here the down projection is in nn.Linear's
  * layout, not channel-major, so that each output channel has a scale.
- * d and f multiples of 16 (else SFN_ERR_MISALIGNED); 1 <= k <= 32, E <= 1024,
- * T k < 2^31 (else SFN_ERR_UNSUPPORTED).  Scratch: at least
+ * d and f multiples of 16 (else SFN_ERR_MISALIGNED) up to 131072; 1 <= k <= 32,
+ * E <= 1024, E d and E f < 2^31, and T k + 16 E rows within the limits of
+ * sfn_matmul_i8 (else SFN_ERR_UNSUPPORTED).  Scratch: at least
  * sfn_experts_i8_workspace_bytes() bytes, 256-byte aligned.
  */
 size_t sfn_experts_i8_workspace_bytes(int64_t T, int E, int k, int d, int f);

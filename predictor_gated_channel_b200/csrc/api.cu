@@ -785,6 +785,9 @@ sfn_status sfn_sparse_ffn_backward(const void *x, const void *A, const void *B, 
 // ------------------------------------------------------------------ experts
 namespace {
 constexpr int kMaxI8K = 131072;  // 127^2 K < 2^31
+// Row and tile numbers of a product are 32-bit: these leave room for the end of the
+// last tile (256 rows) and for a walk's last step (a grid of tiles) past them.
+constexpr int64_t kMaxI8Tiles = 0x7fffffffLL - 8192;
 
 bool dtype_ok(sfn_dtype d) { return d == SFN_DTYPE_BF16 || d == SFN_DTYPE_F32; }
 size_t elt_bytes(sfn_dtype d) { return d == SFN_DTYPE_BF16 ? 2 : 4; }
@@ -800,11 +803,17 @@ sfn_status check_route(sfn_dtype dtype, int64_t T, int E, int k, sfn_score score
   return SFN_OK;
 }
 
-sfn_status check_i8(int64_t T, int N, int K) {
-  if (T < 0 || N <= 0 || K <= 0) return SFN_ERR_INVALID_VALUE;
+sfn_status check_i8_rows(int64_t T, int K) {
+  if (T < 0 || K <= 0) return SFN_ERR_INVALID_VALUE;
   if (K % 16 != 0) return SFN_ERR_MISALIGNED;
-  if (K > kMaxI8K || N > kMaxDi || T > 0x7fffffffLL ||
-      (T + 15) / 16 * ((N + 127) / 128) > 0x7fffffffLL)
+  return K > kMaxI8K || T > 0x7fffffffLL ? SFN_ERR_UNSUPPORTED : SFN_OK;
+}
+
+sfn_status check_i8(int64_t T, int N, int K) {
+  if (N <= 0) return SFN_ERR_INVALID_VALUE;
+  const sfn_status s0 = check_i8_rows(T, K);
+  if (s0 != SFN_OK) return s0;
+  if (N > kMaxDi || T > kMaxI8Tiles || (T + 15) / 16 * ((N + 127) / 128) > kMaxI8Tiles)
     return SFN_ERR_UNSUPPORTED;
   return SFN_OK;
 }
@@ -870,7 +879,7 @@ sfn_status sfn_route_experts_backward(const void *logits, sfn_dtype dtype,
 sfn_status sfn_quantize_rows_i8(const void *x, sfn_dtype dtype, int8_t *q, float *scale,
                                 int64_t T, int K, sfn_stream_t stream) {
   if (!dtype_ok(dtype)) return SFN_ERR_INVALID_VALUE;
-  const sfn_status s0 = check_i8(T, 1, K);
+  const sfn_status s0 = check_i8_rows(T, K);
   if (s0 != SFN_OK) return s0;
   if (T == 0) return SFN_OK;
   if (!x || !q || !scale) return SFN_ERR_INVALID_VALUE;
