@@ -2,12 +2,11 @@
 //
 //   amax = max |x|,  scale = amax / 127,  q = rint(127 x / amax)
 //
-// 127 x is exact for bf16 x (8 + 7 bits of significand), and the quotient is
-// rounded once, so q does not depend on how the quotient is formed: a value
-// half way between two integers (x = amax / 2 is one) is seen as exactly half
-// way and goes to the even one.  A row of zeros has scale 0 and q 0.  A row
-// with an infinity or a NaN has scale NaN and q 0, so that everything
-// computed from it is NaN.
+// q is that integer exactly, for both types: a value half way between two (x =
+// amax / 2 is one) is seen as exactly half way and goes to the even one, and one
+// next to half way to its own side, by the exact remainder.  A row of zeros has
+// scale 0 and q 0.  A row with an infinity or a NaN has scale NaN and q 0, so that
+// everything computed from it is NaN.
 //
 // kRowWarps warps per row hold it in registers, kHeld 16-byte chunks a thread,
 // between the maximum and the quantisation (one read of x); longer rows are read

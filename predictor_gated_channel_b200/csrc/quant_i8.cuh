@@ -22,17 +22,21 @@ __device__ __forceinline__ uint32_t abs_bits_max<EltBF16>(const uint4 &v) {
   return max(m << 16, m & 0xffff0000u);
 }
 
-// What a row's elements are quantised with, from its amax bits.
+// What a row's elements are quantised with, from its amax bits: x pre against
+// amax (which is already times pre).  pre is 1, but a power of two for rows so small
+// or so large that products with 127 or amax, or 127 / amax, would leave the range
+// (an x that it makes a subnormal is far below amax / 254 and quantises to 0).
 struct QuantScale {
-  float amax, mult, scale;
-  bool zero, plain;
+  float amax, mult, scale, pre;
+  bool zero, plain;  // plain: pre is 1
   __device__ __forceinline__ explicit QuantScale(uint32_t bits) {
     amax = __uint_as_float(bits);
     zero = bits == 0u || bits >= 0x7f800000u;
     scale = bits >= 0x7f800000u ? __int_as_float(0x7fc00000) : amax / 127.f;
-    // products with 127 or amax, and 127 / amax, stay well inside the range
-    plain = !zero && amax > 1e-30f && amax < 1e30f;
-    mult = plain ? 127.f / amax : 0.f;
+    pre = amax < 1e-30f ? 0x1p100f : (amax > 1e30f ? 0x1p-100f : 1.f);
+    amax *= pre;
+    plain = !zero && pre == 1.f;
+    mult = 127.f / amax;
   }
 };
 
@@ -47,11 +51,6 @@ struct QuantOut<EltF32> {
   using type = uint32_t;  // 4 values
 };
 
-__device__ __forceinline__ uint32_t pack_i8x4(int a, int b, int c, int d) {
-  return (uint32_t)(a & 0xff) | ((uint32_t)(b & 0xff) << 8) | ((uint32_t)(c & 0xff) << 16) |
-         ((uint32_t)d << 24);
-}
-
 // One value's integer, in the low bits of a float that adding 1.5 * 2^23
 // rounded.  x mult is within 8e-6 of 127 x / amax (|x / amax| <= 1, one
 // rounding of 2^-24), so that both round to the same integer unless it lies
@@ -64,37 +63,57 @@ __device__ __forceinline__ float quantize_fast(float x, float mult, float &near)
   return n;
 }
 
-// Sets that right for a bf16 x, without a division: with n the candidate, the
-// remainder e = 127 x - n amax is exact (127 x and n amax have 15 bits, and for
-// n != 0 their exponents are close), and n moves by one where |e| > amax / 2, or
-// where it is equal and n is odd.  (Exact halves are not rare in bf16: 0.26 %
-// of normal values, some in nearly every row.)
+// Sets that right without a division: with n the candidate, n moves by one where
+// the remainder e = 127 x - n amax has |e| > amax / 2, or where it is equal and n
+// is odd.  (Exact halves are not rare in bf16: 0.26 % of normal values, some in
+// nearly every row.)  Of a bf16 x the remainder is exact: 127 x and n amax have 15
+// bits, and for n != 0 their exponents are close.  Of a float32 x the two products
+// are taken in two parts each, exactly; the difference of the first parts is exact
+// (they are within a factor of two, or n is 0), as is |e| - amax / 2 where it is
+// small, and the second parts have 7 bits each.
+template <class Elt>
 __device__ __forceinline__ float quantize_settle(float x, float n, float amax) {
   const float k = n - kRound;
-  const float e = __fmaf_rn(x, 127.f, -(k * amax));
-  const float over = __fmaf_rn(-0.5f, amax, fabsf(e));
+  float e, over;
+  if (Elt::kBytes == 4) {
+    const float a = 127.f * x, b = k * amax;
+    const float rest = __fmaf_rn(127.f, x, -a) - __fmaf_rn(k, amax, -b);
+    e = a - b;
+    over = __fmaf_rn(-0.5f, amax, fabsf(e)) + (e < 0.f ? -rest : rest);
+  } else {
+    e = __fmaf_rn(x, 127.f, -(k * amax));
+    over = __fmaf_rn(-0.5f, amax, fabsf(e));
+  }
   // over > 0, or over == 0 and the integer is odd
   const bool move = __float_as_int(over) + (int)(__float_as_uint(n) & 1u) > 0;
   return move ? n + copysignf(1.f, e) : n;
 }
 
-// By division, for float32 next to half way and for rows whose amax is so
-// small or so large that the products above leave the range.
+// The integers of four values from the low bits of their floats.
+__device__ __forceinline__ uint32_t pack_low_bytes(const float *n) {
+  uint32_t b[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) b[j] = __float_as_uint(n[j]);
+  return __byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410);
+}
+
+// A chunk of a row whose pre is not 1; not inlined, as it is rare.
 template <class Elt>
-__device__ __noinline__ typename QuantOut<Elt>::type quantize_divide(uint4 v, float amax) {
+__device__ __noinline__ typename QuantOut<Elt>::type quantize_scaled(uint4 v, float amax,
+                                                                     float pre) {
   float f[Elt::kVec];
   Elt::unpack(v, f);
   typename QuantOut<Elt>::type out;
   uint32_t *w = reinterpret_cast<uint32_t *>(&out);
-  // 127 x must not overflow: large rows are scaled by an exact power of two
-  const float pre = amax > 1e36f ? 0.00390625f : 1.f, unit = amax * pre;
+  const float mult = 127.f / amax;
+  float near = 0.f;
 #pragma unroll
-  for (int i = 0; i < Elt::kVec / 4; ++i) {
-    int q[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) q[j] = (int)rintf(127.f * (f[4 * i + j] * pre) / unit);
-    w[i] = pack_i8x4(q[0], q[1], q[2], q[3]);
+  for (int i = 0; i < Elt::kVec; ++i) {
+    f[i] *= pre;
+    f[i] = quantize_settle<Elt>(f[i], quantize_fast(f[i], mult, near), amax);
   }
+#pragma unroll
+  for (int i = 0; i < Elt::kVec / 4; ++i) w[i] = pack_low_bytes(f + 4 * i);
   return out;
 }
 
@@ -110,19 +129,13 @@ __device__ __forceinline__ typename QuantOut<Elt>::type quantize_chunk(const uin
 #pragma unroll
     for (int i = 0; i < Elt::kVec; ++i) n[i] = quantize_fast(f[i], qs.mult, near);
     if (near > kNearHalf) {
-      if (Elt::kBytes == 4) return quantize_divide<Elt>(v, qs.amax);
 #pragma unroll
-      for (int i = 0; i < Elt::kVec; ++i) n[i] = quantize_settle(f[i], n[i], qs.amax);
+      for (int i = 0; i < Elt::kVec; ++i) n[i] = quantize_settle<Elt>(f[i], n[i], qs.amax);
     }
 #pragma unroll
-    for (int i = 0; i < Elt::kVec / 4; ++i) {
-      uint32_t b[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) b[j] = __float_as_uint(n[4 * i + j]);
-      w[i] = __byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410);
-    }
+    for (int i = 0; i < Elt::kVec / 4; ++i) w[i] = pack_low_bytes(n + 4 * i);
   } else if (!qs.zero) {
-    out = quantize_divide<Elt>(v, qs.amax);
+    out = quantize_scaled<Elt>(v, qs.amax, qs.pre);
   }
   return out;
 }

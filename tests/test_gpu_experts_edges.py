@@ -12,7 +12,8 @@ import torch
 import predictor_gated_channel_b200 as sfn
 from predictor_gated_channel_b200 import _capi
 from predictor_gated_channel_b200 import build as sfn_build
-from test_gpu_experts import BF16, DEV, U, expert_weights, rand, ref_route, ref_scores
+from test_gpu_experts import (BF16, DEV, U, expert_weights, rand, ref_quantize, ref_route,
+                              ref_scores)
 
 pytestmark = pytest.mark.gpu
 
@@ -314,3 +315,29 @@ def test_route_by_logits_within_summed_groups(T, E, k, groups, top, score, dtype
     rows = torch.cat([torch.arange(60), torch.arange(T - 30, T)])
     assert np.array_equal(e.cpu()[rows].numpy(),
                           choose_by_logits(logits[rows], k, score, groups, top))
+
+
+# --------------------------------------------------------------- quantisation
+@pytest.mark.parametrize("largest", [1.0, 127.0, 127 * 2.0 ** -9, 254 * 3.0, 0.3, 1e-29, 3.0e38,
+                                     1.3e-38, 1e-31, 2.0 ** -140, 5.1e36])
+def test_quantize_float32_next_to_half_way(largest):
+    """float32 values as close to half way between two integers as they come, on
+    both sides, and exactly half way: the integer of the definition, for every row
+    length's kernel.  (The reference divides in float64, whose rounding of 2^-46 is
+    far below the 2^-33 that a quotient is away from half way if it is not on it.)"""
+    amax = torch.tensor(largest, dtype=torch.float32)
+    halves = (torch.arange(-127, 127).double() + 0.5) * amax.double() / 127
+    x = halves.float()
+    near = [x, torch.nextafter(x, torch.tensor(math.inf)), torch.nextafter(x, -torch.tensor(math.inf))]
+    near += [torch.nextafter(near[1], torch.tensor(math.inf)), amax[None],
+             (torch.arange(-127, 128).double() * amax.double() / 127).float()]
+    values = torch.cat(near)
+    values = values[values.abs() <= amax]
+    for K in (64, 1024, 4096, 40960):
+        g = torch.Generator().manual_seed(K)
+        rows = max(3, 4000 // K)
+        row = values[torch.randint(0, values.numel(), (rows, K), generator=g)]
+        row[:, 3] = -amax
+        q, s = sfn.quantize_rows_i8(row.to(DEV))
+        rq, _ = ref_quantize(row)
+        assert torch.equal(q.cpu().double(), rq)
