@@ -429,12 +429,12 @@ __global__ void __launch_bounds__(kThreads)
   if (threadIdx.x < slots) {
     const int e = experts[threadIdx.x];
     ids[threadIdx.x] = (e >= 0 && e < E) ? e : -1;
-    slot_weight[threadIdx.x] = weights[threadIdx.x];
   }
   if (threadIdx.x < kGemvSlots) amax[threadIdx.x] = 0u;
   __syncthreads();
   stream_rows<1>(
       units * k, f, acc, smem, bars, err, DownRows{Wd, hq, ids, u0, f, d, k}, [&] {
+        if (threadIdx.x < slots) slot_weight[threadIdx.x] = weights[threadIdx.x];
         for (int i = threadIdx.x; i < units * k; i += kThreads) {
           const int u = u0 + i / k, s = u / d * k + i % k;
           acc[i] = 0;

@@ -57,12 +57,13 @@ __device__ __forceinline__ void top8(const uint32_t (&w)[V], uint32_t (&top)[8])
 // Eight lanes per row, four rows a warp, k <= 8: for many rows, where the
 // instructions that do not depend on E (picks, weights, stores, loop) count;
 // four rows share them.  V = E / 8 values a lane, neighbours with kGroups (8
-// lanes are then a whole number for each group), else every eighth.  A row with
+// lanes are then a whole number for each group; by logit only), else every eighth.  A row with
 // anything to settle (a NaN, neighbours or a k-th place within the words or the
 // error bound, more than eight of one lane) is left to the whole warp.
 template <bool kBf16, int V, bool kByLogit, bool kGroups>
 __global__ void __launch_bounds__(32 * kWarps, (lanes_blocks<V, kByLogit>()))
     k_route_lanes(const RouteParams p) {
+  static_assert(kByLogit || !kGroups, "groups are ranked by their largest logit here");
   extern __shared__ double route_smem[];
   pdl_wait();
   pdl_launch_dependents();
@@ -121,27 +122,15 @@ __global__ void __launch_bounds__(32 * kWarps, (lanes_blocks<V, kByLogit>()))
     const float most = p.sigmoid || kByLogit ? 1.f : (z_fast > 0.f ? __fdividef(1.f, z_fast) : 0.f);
     auto bound = [&](float x) { return score_error(most, x, p.sigmoid); };
     bool unsure = nan || (!kByLogit && !number), in = true;
-    if (kGroups) {
-      float a = -INFINITY, b = -INFINITY;
+    if (kGroups) {  // by their largest logit
+      float gs = -INFINITY;
 #pragma unroll
-      for (int j = 0; j < V; ++j) {
-        b = fmaxf(b, fminf(a, c[j]));
-        a = fmaxf(a, c[j]);
-      }
-      for (int o = per >> 1; o > 0; o >>= 1) {
-        const float a2 = __shfl_xor_sync(kFull, a, o), b2 = __shfl_xor_sync(kFull, b, o);
-        b = fmaxf(fmaxf(b, b2), fminf(a, a2));
-        a = fmaxf(a, a2);
-      }
-      const float gs = (p.group_top == 2 && b != -INFINITY) ? a + b : a;
+      for (int j = 0; j < V; ++j) gs = fmaxf(gs, c[j]);
+      for (int o = per >> 1; o > 0; o >>= 1) gs = fmaxf(gs, __shfl_xor_sync(kFull, gs, o));
       int rank = 0;
       for (int o = per; o < kRowLanes; o += per) {
         const float other = __shfl_xor_sync(kFull, gs, o);
         rank += other > gs || (other == gs && (sub ^ o) / per < sub / per);
-        if (!kByLogit)
-          unsure |= gs > -INFINITY && other > -INFINITY &&
-                    fabsf(gs - other) <= 2.f * (bound(gs) + bound(other)) +
-                                             4.f * kUlp * (fabsf(gs) + fabsf(other));
       }
       in = rank < p.top_groups;
     }

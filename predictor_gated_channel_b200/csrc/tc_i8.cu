@@ -599,7 +599,7 @@ bool map_i8(CUtensorMap *m, const void *base, uint64_t k, uint64_t rows, uint32_
 }
 
 // Stages of the ring and the kernel's shared memory.
-size_t ring(I8Params &p, int num_w) {
+size_t ring(I8Params &p) {
   // alignment slack, barriers, the groups' offsets
   const size_t fixed = 1024 + (2 * kMaxStages + 5) * 8 + 16 +
                        (p.offsets ? (size_t)(p.groups + 1) * sizeof(int) : 0);
@@ -612,7 +612,7 @@ size_t ring(I8Params &p, int num_w) {
 template <bool kSwiGlu, Out kOut, Span kSpan>
 cudaError_t launch(const CUtensorMap &tX, const CUtensorMap &tW, const CUtensorMap &tW2,
                    I8Params p, int64_t units, int cluster, int num_sms, cudaStream_t st) {
-  const size_t smem = ring(p, kSwiGlu ? 2 : 1);
+  const size_t smem = ring(p);
   if (p.stages < 2) return cudaErrorInvalidValue;
   auto kern = k_i8_gemm<kSwiGlu, kOut, kSpan>;
   const cudaError_t e = ensure_smem_limit(reinterpret_cast<const void *>(kern), smem);
