@@ -4,11 +4,16 @@
 namespace sfn {
 namespace {
 
-// Eight lanes a row instead of a warp: 32768 x 160 bf16 11.5 us against 18.4,
-// 8192 x 64 3.6 against 6.1, 2048 x 160 3.0 against 3.2; float32 32768 x 160 13.3
-// against 24.1.  With a bias, where rows may be left to the whole warp, for many
-// rows only: 32768 x 64 20.8 us against 30.0, but 4096 x 256 in groups 15.6
-// against 11.0.
+// Eight lanes a row instead of a warp, k 8, us at 512 / 2048 / 8192 / 32768 rows.
+// By logit: bf16 64 experts 3.1 / 3.3 / 4.2 / 8.1 against 3.0 / 3.5 / 6.4 / 15.4, 160
+// 3.5 / 3.5 / 5.0 / 11.8 against 3.1 / 4.0 / 7.1 / 20.3, 256 4.0 / 4.1 / 6.4 / 15.7
+// against 2.9 / 3.9 / 7.2 / 21.9; float32 192 4.2 / 5.1 / 6.7 / 17.6 against 3.4 / 4.5 /
+// 8.5 / 27.0 (the worst at 2048); in 8 groups 256 5.1 / 5.5 / 9.0 / 20.5 against 3.9 /
+// 5.5 / 12.1 / 38.3.  With a bias, where rows may be left to the whole warp, the two
+// meet later: at 2048 / 8192 / 16384 / 32768 rows 64 experts 6.7 / 8.0 / 12.1 / 15.6
+// against 5.0 / 8.9 / 14.7 / 25.0, 128 8.2 / 11.2 / 13.7 / 21.5 against 5.4 / 10.1 / 16.0 /
+// 29.7, 192 10.4 / 13.7 / 19.4 / 33.6 against 6.0 / 12.1 / 20.2 / 38.9, 256 10.0 / 13.5 /
+// 20.3 / 34.1 against 6.5 / 14.1 / 22.8 / 41.4.
 bool by_lanes(const RouteParams &p, bool by_logit) {
   if (p.k > 8 || p.scores != nullptr || p.E > 256) return false;
   if (p.groups > 1)  // a lane's values are neighbours, as many as are built

@@ -32,11 +32,10 @@
 // What the rare paths cost is their latency, at the end of a launch: each
 // level (words, whole scores, float64 of the slots and the next two, float64 of
 // the row) is there so that few rows see the next.
-//   4096 x 256, 8 groups: 11.0 us (of it 3 us of rows decided in float64); 22.5
-//   us with whole keys alone (2557 instructions a row), 20.9 us with float64 rows
-//   in place of float64 slots
-//   32768 x 160, bf16: 18.4 us (356 instructions a row), 11.5 us with eight lanes
-//   a row (route_lanes.cu); 38.9 us with whole keys
+//   4096 x 256, 8 groups: 10.7 us (of it 3 us of rows decided in float64); 22.5
+//   us with whole keys alone, 20.9 us with float64 rows in place of float64 slots
+//   32768 x 160, bf16, k 6: 18.4 us, 11.7 us with eight lanes a row
+//   (route_lanes.cu); 38.9 us with whole keys
 #pragma once
 
 #include <cmath>
@@ -380,12 +379,17 @@ __device__ __forceinline__ float row_sum(const float (&l)[V], float m) {
   return z;
 }
 
-// Blocks of kWarps rows an SM holds at once (the launch bound and the grid).
-// Seven for 256 experts, so that 4096 rows are one wave: 11.0 us; six, with the
-// next row's logits loaded ahead, 13.8 us.
-template <int V>
+// Blocks of kWarps rows an SM holds at once (the launch bound and the grid): as
+// many as the registers allow without spills on the usual path; the kernels that
+// rank by logit need fewer of them.  us, k 8.  By score, 7 blocks (V <= 4) or 5 (V <=
+// 8) against 8 or 7: 128 experts, 512 / 4096 / 8192 rows 3.9 / 7.1 / 10.1 against 4.3 /
+// 7.5 / 10.6; 256 4.4 / 9.0 / 13.9 against 5.0 / 9.3 / 13.9; 256 in 8 groups, 512 / 4096 /
+// 32768 rows 5.0 / 10.7 / 52.1 against 5.9 / 11.7 / 58.8.  By logit, 7 against 5: 192
+// in 8 groups 3.9 / 6.9 / 34.0 against 3.9 / 7.2 / 39.5.
+template <int V, bool kByLogit>
 constexpr int route_blocks() {
-  return V <= 4 ? 8 : (V <= 8 ? 7 : (V <= 16 ? 4 : 2));
+  if (kByLogit) return V <= 4 ? 8 : (V <= 8 ? 7 : (V <= 16 ? 4 : 2));
+  return V <= 4 ? 7 : (V <= 8 ? 5 : (V <= 16 ? 4 : 2));
 }
 
 // Mask of a value's place among a lane's V, in the low bits of a packed word.
@@ -394,14 +398,20 @@ constexpr uint32_t places() {
   return V <= 1 ? 0u : V <= 2 ? 1u : V <= 4 ? 3u : V <= 8 ? 7u : V <= 16 ? 15u : 31u;
 }
 
-// As route_blocks(), of the kernels with eight lanes a row.  Seven of 16 values
-// make 32768 rows two rounds of the warps in place of three (128 experts, bf16:
-// 10.9 to 9.6 us for the gradient); with more values only the kernels that need
-// few registers gain (160 experts by logit 14.6 to 11.5 us; the gradient of 256
-// would spill, 8.9 to 9.5).
-template <int V, bool kFewRegisters>
+// As route_blocks(), of the kernels with eight lanes a row.  By score five of V <=
+// 16 against seven and eight: 16384 / 32768 rows of 64 experts 11.8 / 15.3 us against
+// 12.7 / 17.9, of 128 13.6 / 21.3 against 16.0 / 25.6; four of more values against
+// three: of 256 20.3 / 34.2 against 22.4 / 36.1.  By logit eight and seven against six
+// and five: 8192 / 32768 rows of 64 4.6 / 9.7 us against 4.6 / 9.6, of 128 5.1 / 12.0
+// against 5.5 / 12.6, of 160 6.0 / 13.7 against 6.1 / 15.1, of 256 7.5 / 17.8 against
+// 8.1 / 20.3.  The dense gradient: 64 4.4 / 8.8 against 4.5 / 10.0 (six), 128 6.5 /
+// 14.1 against 7.0 / 15.6 (five), 256 with four 11.5 / 35.8 against 14.8 / 37.0 (three).
+enum class Lanes { kByLogit, kByScore, kGradient };
+template <int V, Lanes kKind>
 constexpr int lanes_blocks() {
-  return V <= 8 ? 8 : (V <= 16 || kFewRegisters ? 7 : 4);
+  if (kKind == Lanes::kByLogit) return V <= 8 ? 8 : 7;
+  if (kKind == Lanes::kByScore) return V <= 16 ? 5 : 4;
+  return V <= 8 ? 8 : (V <= 16 ? 7 : 4);
 }
 
 // Among a row's eight lanes.

@@ -236,7 +236,7 @@ __global__ void __launch_bounds__(32 * kWarps, backward_blocks<V>())
 // without their slots, then, after a warp barrier, each slot's whole gradient
 // over them by a lane of its own.
 template <bool kBf16, int V, bool kBlocked>
-__global__ void __launch_bounds__(32 * kWarps, (lanes_blocks<V, false>()))
+__global__ void __launch_bounds__(32 * kWarps, (lanes_blocks<V, Lanes::kGradient>()))
     k_route_bwd_lanes(const RouteBwdParams p) {
   pdl_wait();
   pdl_launch_dependents();
@@ -351,7 +351,7 @@ cudaError_t launch_route_backward(const RouteShape &s, const void *logits,
     auto go = [&](auto v) {
       constexpr int V = decltype(v)::value;
       auto launch = [&](auto *kern) {
-        return launch_rows(kern, (s.T + 3) / 4, lanes_blocks<V, false>(), 0, num_sms, st, p);
+        return launch_rows(kern, (s.T + 3) / 4, lanes_blocks<V, Lanes::kGradient>(), 0, num_sms, st, p);
       };
       const bool blocked = vectors && s.E == kRowLanes * V;
       if (s.bf16)

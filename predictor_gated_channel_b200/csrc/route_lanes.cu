@@ -54,6 +54,11 @@ __device__ __forceinline__ void top8(const uint32_t (&w)[V], uint32_t (&top)[8])
   }
 }
 
+template <bool kByLogit>
+constexpr Lanes route_kind() {
+  return kByLogit ? Lanes::kByLogit : Lanes::kByScore;
+}
+
 // Eight lanes per row, four rows a warp, k <= 8: for many rows, where the
 // instructions that do not depend on E (picks, weights, stores, loop) count;
 // four rows share them.  V = E / 8 values a lane, neighbours with kGroups (8
@@ -61,7 +66,7 @@ __device__ __forceinline__ void top8(const uint32_t (&w)[V], uint32_t (&top)[8])
 // anything to settle (a NaN, neighbours or a k-th place within the words or the
 // error bound, more than eight of one lane) is left to the whole warp.
 template <bool kBf16, int V, bool kByLogit, bool kGroups>
-__global__ void __launch_bounds__(32 * kWarps, (lanes_blocks<V, kByLogit>()))
+__global__ void __launch_bounds__(32 * kWarps, (lanes_blocks<V, route_kind<kByLogit>()>()))
     k_route_lanes(const RouteParams p) {
   static_assert(kByLogit || !kGroups, "groups are ranked by their largest logit here");
   extern __shared__ double route_smem[];
@@ -253,7 +258,7 @@ cudaError_t launch_route_lanes(const RouteParams &p, bool by_logit, int num_sms,
     auto launch = [&](auto logit, auto grouped) {
       return launch_rows(
           k_route_lanes<kBf16, V, decltype(logit)::value, decltype(grouped)::value>,
-          (p.T + 3) / 4, lanes_blocks<V, decltype(logit)::value>(), smem, num_sms, st, p);
+          (p.T + 3) / 4, lanes_blocks<V, route_kind<decltype(logit)::value>()>(), smem, num_sms, st, p);
     };
     if (groups) return launch(std::true_type{}, std::true_type{});
     return by_logit ? launch(std::true_type{}, std::false_type{})

@@ -9,7 +9,8 @@ namespace {
 
 // One warp per row.
 template <bool kBf16, int V, bool kBlocked, bool kByLogit, bool kGroups>
-__global__ void __launch_bounds__(32 * kWarps, route_blocks<V>()) k_route(const RouteParams p) {
+__global__ void __launch_bounds__(32 * kWarps, (route_blocks<V, kByLogit>()))
+    k_route(const RouteParams p) {
   extern __shared__ double route_smem[];
   pdl_wait();
   pdl_launch_dependents();
@@ -90,7 +91,7 @@ cudaError_t launch_route_warps(const RouteParams &p, bool by_logit, int num_sms,
         return cudaErrorInvalidValue;
       else
         return launch_rows(k_route<kBf16, V, kB, decltype(logit)::value, decltype(grouped)::value>,
-                           p.T, route_blocks<V>(), smem, num_sms, st, p);
+                           p.T, route_blocks<V, decltype(logit)::value>(), smem, num_sms, st, p);
     };
     auto with_groups = [&](auto logit) {
       return groups ? go(logit, std::true_type{}) : go(logit, std::false_type{});
