@@ -86,8 +86,9 @@ __device__ __forceinline__ float swiglu_f32(float g, float u) {
 }
 #endif
 
-// For a few slots (T k <= kGemvSlots): gate/up and down as streams of the
-// slots' weight rows, each slot on its own.  h is [T k][f] in slot order.
+// For a few slots (T k <= kGemvSlots, what a warp's lanes hold): gate/up and down
+// as streams of the slots' weight rows, each slot on its own.  h is [T k][f] in slot
+// order.
 constexpr int kGemvSlots = 32;
 bool experts_gemv_ok(const ExpertShape &s, int num_sms);
 cudaError_t launch_experts_gemv_gateup(const ExpertShape &s, const DeviceInfo &dev, const void *x,

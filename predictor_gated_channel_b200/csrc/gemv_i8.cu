@@ -518,10 +518,23 @@ cudaError_t launch_linear_gemv(const I8Shape &s, bool x_bf16, const DeviceInfo &
   return x_bf16 ? with_tok(EltBF16{}) : with_tok(EltF32{});
 }
 
+// A slot streams its expert's weights by itself, also where another slot has the
+// same expert: tiles read them once, but take three or four launches more.  us with
+// streams against tiles: 16 experts of 4096 x 1792, 1 / 4 / 16 slots 15.5 / 26.5 /
+// 68.7 against 44.2 / 50.6 / 78.9; 8 of 2048 x 4096 15.7 / 24.7 / 57.8 against 41.8 /
+// 44.9 / 63.8; 64 of 1024 x 512, 8 / 32 slots 14.4 / 26.7 against 43.4 / 46.3.  The
+// weights that slots have in common cost more than that from about 200 MB on: 2
+// experts of 4096 x 1792, 8 / 12 / 32 slots 29.8 / 40.3 / 86.6 against 43.0 / 43.4 /
+// 42.0 (132, 220, 660 MB); 8 experts, 16 / 24 slots 52.0 / 95.5 against 58.1 / 60.5
+// (176, 352 MB); 1 of 2048 x 4096, 8 / 12 slots 31.8 / 44.6 against 38.9 / 38.7 (176,
+// 277 MB).
+constexpr int64_t kGemvAgain = 200'000'000;
 bool experts_gemv_ok(const ExpertShape &s, int num_sms) {
   if (s.slots() > kGemvSlots || s.slots() * s.f * 2 > 0x7fffffffLL ||
       s.slots() * s.d > 0x7fffffffLL)
     return false;
+  const int64_t again = s.slots() - (s.slots() < s.E ? s.slots() : s.E);
+  if (again * 3 * s.d * s.f > kGemvAgain) return false;
   return gateup_layout(s, num_sms).total <= kSmemMost &&
          down_layout(s, num_sms).total <= kSmemMost;
 }

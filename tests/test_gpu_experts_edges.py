@@ -341,3 +341,22 @@ def test_quantize_float32_next_to_half_way(largest):
         q, s = sfn.quantize_rows_i8(row.to(DEV))
         rq, _ = ref_quantize(row)
         assert torch.equal(q.cpu().double(), rq)
+
+
+@pytest.mark.parametrize("T,E,k,d,f", [(8, 2, 2, 4096, 1792), (16, 2, 2, 4096, 1792),
+                                       (8, 1, 1, 2048, 4096), (12, 1, 1, 2048, 4096),
+                                       (3, 8, 8, 4096, 1792)])
+def test_experts_that_slots_share(T, E, k, d, f):
+    """Few slots, several of the same expert: streams up to some bytes of weights
+    read again, tiles past them, with the same bits as a token by itself."""
+    W = expert_weights(T, E, f, d)
+    x = rand(T, T, d).to(torch.bfloat16).to(DEV)
+    g = torch.Generator().manual_seed(T)
+    experts = torch.stack([torch.randperm(E, generator=g)[:k] for _ in range(T)])
+    experts = experts.to(torch.int32).to(DEV)
+    weights = torch.rand((T, k), generator=g).to(DEV)
+    y = sfn.experts_i8_forward(x, experts, weights, **W)
+    for t in (0, T // 2, T - 1):
+        one = sfn.experts_i8_forward(x[t:t + 1], experts[t:t + 1].contiguous(),
+                                     weights[t:t + 1].contiguous(), **W)
+        assert torch.equal(one, y[t:t + 1])
