@@ -50,7 +50,7 @@ __global__ void __launch_bounds__(32 * kWarps, (route_blocks<V, kByLogit>()))
     const int pick = select_row<kBf16, V, kBlocked, kByLogit, kGroups>(
         p, t, l, bias, nan, m, z_fast, route_smem + (size_t)warp * (kGroups ? p.E : 0), lp, bp);
     const bool slot = lane < p.k;
-    if (bp == -INFINITY) lp = -INFINITY;
+    if (!slot || bp == -INFINITY) lp = -INFINITY;  // (the choice may leave more than k)
     const bool empty = lp == -INFINITY;
     float w;
     if (p.renorm) {

@@ -360,3 +360,26 @@ def test_experts_that_slots_share(T, E, k, d, f):
         one = sfn.experts_i8_forward(x[t:t + 1], experts[t:t + 1].contiguous(),
                                      weights[t:t + 1].contiguous(), **W)
         assert torch.equal(one, y[t:t + 1])
+
+
+@pytest.mark.parametrize("size", [2.0 ** 40, 2.0 ** 100])
+@pytest.mark.parametrize("T", [9, 2100, 17000])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_route_weights_beside_a_larger_logit_next_in_line(T, score, size):
+    """Experts that the selection scores leave out by a tie (a bias that swallows
+    the scores, in float32 or in float64 too), with logits far above the chosen:
+    the weights are the chosen ones' alone."""
+    E, k = 64, 4
+    logits = rand(T, T, E) - (150.0 if score == "sigmoid" else 0.0)
+    logits[:, 4:6] += 150.0
+    for groups, others in ((1, size), (8, size), (1, 0.0)):
+        bias = torch.full((E,), size)
+        bias[6:] = others
+        e, w, _ = sfn.route_experts(logits.to(DEV), k, bias=bias.to(DEV), score=score,
+                                    groups=groups, top_groups=groups)
+        re, rw, _ = ref_route(logits[:9], k, bias, score, groups, groups)
+        assert np.array_equal(e.cpu()[:9].numpy(), re)
+        # float64 tells scores beside 2^40 apart, but not beside 2^100
+        assert size == 2.0 ** 40 or (e == torch.arange(4, device=DEV)).all()
+        assert np.allclose(w.cpu()[:9].double().numpy(), rw, rtol=100 * U, atol=1e-37)
+        assert ((w.sum(1) - 1).abs() < 1e-5).all()
