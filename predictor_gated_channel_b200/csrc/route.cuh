@@ -359,14 +359,22 @@ __device__ __forceinline__ void load_row(const void *logits, int64_t t, int E, f
   }
 }
 
-// Maximum over the row (NaN ignored) and, given it, the sum of exponentials.
+// Maximum over the row (nan: it has a NaN, and so is the maximum) and, given it,
+// the sum of exponentials.
 template <int V>
-__device__ __forceinline__ float row_max(const float (&l)[V]) {
+__device__ __forceinline__ float row_max(const float (&l)[V], bool nan) {
   float m = l[0];
 #pragma unroll
   for (int j = 1; j < V; ++j) m = fmaxf(m, l[j]);
   const uint32_t key = __reduce_max_sync(kFull, order_key(m));
-  return key == 0u ? -INFINITY : key_value(key);
+  return nan ? __int_as_float(0x7fc00000) : key_value(key);
+}
+template <int V>
+__device__ __forceinline__ bool row_has_nan(const float (&l)[V]) {
+  bool nan = false;
+#pragma unroll
+  for (int j = 0; j < V; ++j) nan |= l[j] != l[j];
+  return __any_sync(kFull, nan);
 }
 template <int V, bool kFast>
 __device__ __forceinline__ float row_sum(const float (&l)[V], float m) {
@@ -458,17 +466,15 @@ __device__ __noinline__ int settle_row(const RouteParams &p, int64_t t, double *
   } else {
     const bool by_l = p.bias == nullptr;
     float bias[V];
-    bool nan = false;
 #pragma unroll
     for (int j = 0; j < V; ++j) {
       const int e = expert_of<V, false>(j);
       bias[j] = (p.bias != nullptr && e < p.E) ? __ldg(p.bias + e) : 0.f;
-      nan |= l[j] != l[j];
     }
-    nan = __any_sync(kFull, nan);
+    const bool nan = row_has_nan<V>(l);
     float m = 0.f, z = 1.f;
     if (!p.sigmoid) {
-      m = row_max<V>(l);
+      m = row_max<V>(l, nan);
       z = row_sum<V, true>(l, m);
     }
     if (!nan) {

@@ -134,7 +134,7 @@ __global__ void __launch_bounds__(32 * kWarps, backward_blocks<V>())
     float m = 0.f;
     bool bad = false;
     if constexpr (kLogits && !kDense) {
-      m = row_max<V>(l);
+      m = row_max<V>(l, false);
 #pragma unroll
       for (int j = 0; j < V; ++j) bad |= !(l[j] < INFINITY);
       bad = __any_sync(kFull, bad);
@@ -142,7 +142,7 @@ __global__ void __launch_bounds__(32 * kWarps, backward_blocks<V>())
     if constexpr (kDense) {
       if (!p.sigmoid) {
         // l becomes the row's scores
-        m = row_max<V>(l);
+        m = row_max<V>(l, row_has_nan<V>(l));
         float z = 0.f;
 #pragma unroll
         for (int j = 0; j < V; ++j) {
@@ -273,11 +273,12 @@ __global__ void __launch_bounds__(32 * kWarps, (lanes_blocks<V, Lanes::kGradient
 #pragma unroll
       for (int j = 1; j < V; ++j) m = fmaxf(m, l[j]);
       const uint32_t key = lanes_max(order_key(m));
-      m = key == 0u ? -INFINITY : key_value(key);
+      m = key_value(key);
       float z = 0.f;
 #pragma unroll
       for (int j = 0; j < V; ++j) {
-        l[j] = m == -INFINITY ? 0.f : expf(l[j] - m);  // l becomes the scores
+        // l becomes the scores; a NaN stays one and makes all of them NaN
+        l[j] = m == -INFINITY && l[j] == m ? 0.f : expf(l[j] - m);
         z += l[j];
       }
       z = lanes_add(z);

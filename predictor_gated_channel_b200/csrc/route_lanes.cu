@@ -9,10 +9,7 @@ template <bool kBf16, int V, bool kBlocked, bool kByLogit, bool kGroups>
 __device__ __noinline__ int select_left_row(const RouteParams &p, int64_t t, double *row64) {
   float l[V], bias[kByLogit ? 1 : V];
   load_row<kBf16, V, kBlocked>(p.logits, t, p.E, l);
-  bool nan = false;
-#pragma unroll
-  for (int j = 0; j < V; ++j) nan |= l[j] != l[j];
-  nan = __any_sync(kFull, nan);
+  const bool nan = row_has_nan<V>(l);
   float m = 0.f, z = 1.f, lp, bp;
   if constexpr (!kByLogit) {
 #pragma unroll
@@ -21,7 +18,7 @@ __device__ __noinline__ int select_left_row(const RouteParams &p, int64_t t, dou
       bias[j] = (p.bias != nullptr && e < p.E) ? __ldg(p.bias + e) : 0.f;
     }
     if (!p.sigmoid) {
-      m = row_max<V>(l);
+      m = row_max<V>(l, nan);
       z = row_sum<V, true>(l, m);
     }
   }

@@ -27,16 +27,13 @@ __global__ void __launch_bounds__(32 * kWarps, (route_blocks<V, kByLogit>()))
   for (int64_t t = (int64_t)blockIdx.x * kWarps + warp; t < p.T; t += stride) {
     float l[V];
     load_row<kBf16, V, kBlocked>(p.logits, t, p.E, l);
-    bool nan = false;
-#pragma unroll
-    for (int j = 0; j < V; ++j) nan |= l[j] != l[j];
-    nan = __any_sync(kFull, nan);
+    const bool nan = row_has_nan<V>(l);
     // softmax statistics, where something needs every score: z_fast for the
     // choice, z for what is written
     float m = 0.f, z = 1.f, z_fast = 1.f;
     const bool exact_z = !p.sigmoid && (p.scores != nullptr || !p.renorm);
     if (!p.sigmoid && (!kByLogit || exact_z)) {
-      m = row_max<V>(l);
+      m = row_max<V>(l, nan);
       if (!kByLogit) z_fast = row_sum<V, true>(l, m);
       if (exact_z) z = row_sum<V, false>(l, m);
     }

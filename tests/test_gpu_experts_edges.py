@@ -383,3 +383,36 @@ def test_route_weights_beside_a_larger_logit_next_in_line(T, score, size):
         assert size == 2.0 ** 40 or (e == torch.arange(4, device=DEV)).all()
         assert np.allclose(w.cpu()[:9].double().numpy(), rw, rtol=100 * U, atol=1e-37)
         assert ((w.sum(1) - 1).abs() < 1e-5).all()
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("T,E", [(12, 64), (12, 33), (12, 600), (9000, 64), (17000, 100)])
+def test_route_softmax_rows_of_nothing_but_nan(T, E, dtype):
+    """A NaN makes its row's scores NaN also where nothing else is left of it: all
+    NaN, or NaN and masked experts (which, at -inf, rank above a NaN and are empty
+    slots).  With a bias and without, scores written, and the dense gradient."""
+    k = 3
+    logits = rand(T, T, E).to(dtype)
+    logits[1] = math.nan
+    logits[4] = -math.inf
+    logits[4, 7] = math.nan
+    logits[9, 5] = math.nan
+    bad = [1, 4, 9]
+    good = torch.ones(T, dtype=torch.bool)
+    good[bad] = False
+    for bias in (None, torch.linspace(0, 1, E)):
+        b = None if bias is None else bias.to(DEV)
+        for renorm in (False, True):
+            for want in (False, True):
+                e, w, s = sfn.route_experts(logits.to(DEV), k, bias=b, renormalize=renorm,
+                                            want_scores=want)
+                assert e[1].tolist() == [0, 1, 2] and (e[4] == -1).all()
+                assert torch.isnan(w[1]).all() and (w[4] == 0).all() and torch.isnan(w[9]).all()
+                assert torch.isfinite(w[good]).all()
+                if want:
+                    assert torch.isnan(s[bad]).all() and torch.isfinite(s[good]).all()
+            dw, ds = rand(5, T, k).to(DEV), rand(6, T, E).to(DEV)
+            got = sfn.route_experts_backward(logits.to(DEV), e, dw, dscores=ds, renormalize=renorm)
+            assert torch.isnan(got[bad]).all() and torch.isfinite(got[good]).all()
+            got = sfn.route_experts_backward(logits.to(DEV), e, dw, renormalize=renorm)
+            assert torch.isnan(got[bad]).all() and torch.isfinite(got[good]).all()
