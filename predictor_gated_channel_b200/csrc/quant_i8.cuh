@@ -76,12 +76,13 @@ __device__ __forceinline__ float quantize_settle(float x, float n, float amax) {
   const float k = n - kRound;
   float e, over;
   if (Elt::kBytes == 4) {
-    const float a = 127.f * x, b = k * amax;
-    const float rest = __fmaf_rn(127.f, x, -a) - __fmaf_rn(k, amax, -b);
-    e = a - b;
-    over = __fmaf_rn(-0.5f, amax, fabsf(e)) + (e < 0.f ? -rest : rest);
+    // (named roundings: fused into the difference, a product would be taken whole)
+    const float a = __fmul_rn(127.f, x), b = __fmul_rn(k, amax);
+    const float rest = __fsub_rn(__fmaf_rn(127.f, x, -a), __fmaf_rn(k, amax, -b));
+    e = __fsub_rn(a, b);
+    over = __fadd_rn(__fmaf_rn(-0.5f, amax, fabsf(e)), e < 0.f ? -rest : rest);
   } else {
-    e = __fmaf_rn(x, 127.f, -(k * amax));
+    e = __fmaf_rn(x, 127.f, -__fmul_rn(k, amax));
     over = __fmaf_rn(-0.5f, amax, fabsf(e));
   }
   // over > 0, or over == 0 and the integer is odd

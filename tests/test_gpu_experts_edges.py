@@ -13,7 +13,7 @@ import predictor_gated_channel_b200 as sfn
 from predictor_gated_channel_b200 import _capi
 from predictor_gated_channel_b200 import build as sfn_build
 from test_gpu_experts import (BF16, DEV, U, expert_weights, rand, ref_quantize, ref_route,
-                              ref_scores)
+                              ref_scores, weights_i8)
 
 pytestmark = pytest.mark.gpu
 
@@ -341,6 +341,31 @@ def test_quantize_float32_next_to_half_way(largest):
         q, s = sfn.quantize_rows_i8(row.to(DEV))
         rq, _ = ref_quantize(row)
         assert torch.equal(q.cpu().double(), rq)
+
+
+@pytest.mark.parametrize("T,K,N", [(1, 64, 40), (2, 1088, 135), (3, 4096, 64), (4, 7344, 126),
+                                   (2, 8400, 541), (1, 40960, 16)])
+def test_few_tokens_quantise_as_many_do(T, K, N):
+    """float32 tokens of values next to half way between two integers: the stream
+    of few tokens, which quantises in its own kernel, has the integers of the
+    definition too (the products are then the same bits)."""
+    g = torch.Generator().manual_seed(K)
+    amax = torch.rand(T, 1, generator=g) * 5 + 0.1
+    halves = (torch.randint(-127, 127, (T, K), generator=g).double() + 0.5) * amax.double() / 127
+    x = halves.float()
+    away = torch.where(torch.rand(T, K, generator=g) < 0.5, math.inf, -math.inf)
+    x = torch.where(torch.rand(T, K, generator=g) < 0.5, torch.nextafter(x, away), x)
+    x = x.clamp(-amax, amax)
+    x[:, :1] = amax
+    wq, sw = weights_i8(5, N, K)
+    rq, rs = ref_quantize(x)
+    q, s = sfn.quantize_rows_i8(x.to(DEV))
+    assert torch.equal(q.cpu().double(), rq)
+    y = sfn.linear_i8(x.to(DEV), wq.to(DEV), sw.to(DEV))
+    assert torch.equal(y, sfn.matmul_i8(q, s, wq.to(DEV), sw.to(DEV), out_dtype=torch.float32))
+    ref = (rq @ wq.double().T) * rs[:, None] * sw.double()
+    # the exact sum's conversion and two scalings, and the scale's own rounding
+    assert ((y.cpu().double() - ref).abs() <= 5 * U * ref.abs()).all()
 
 
 @pytest.mark.parametrize("T,E,k,d,f", [(8, 2, 2, 4096, 1792), (16, 2, 2, 4096, 1792),
