@@ -82,7 +82,8 @@ cudaError_t launch_i8_experts_down(const ExpertShape &s, const DeviceInfo &dev,
 // experts of 4096 x 1792 with 512 rows each.
 #ifdef __CUDACC__
 __device__ __forceinline__ float swiglu_f32(float g, float u) {
-  return __fdiv_rn(g, 1.f + expf(-g)) * u;
+  // (named roundings: fused in one kernel and not in the other, bits would differ)
+  return __fmul_rn(__fdiv_rn(g, __fadd_rn(1.f, expf(-g))), u);
 }
 #endif
 
