@@ -14,11 +14,11 @@
 // across row boundaries.  Each warp keeps a ring of its own in shared memory
 // that bulk copies fill kStages pieces ahead: 128 KB in flight per SM, as 32
 // warps x 2 x 2 KB.  Measured on the 8-of-64 experts of 4096 x 1792, one token:
-// 36.9 us; a third stage 42.5 us, pieces of 1 KB 46 us, the pieces dealt round
-// robin 39.4 us; the pieces held in registers instead, eight loads ahead, 90 us
-// (a warp has too few load scoreboards to wait for one of many).  The stream
-// runs at the rate of memory (58.7 MB in 8.6 us); what is left is 4.6 us a
-// kernel: its launch, the rows' quantisation, the last sums.
+// 37.4 us (when it took 36.9: a third stage 42.5 us, pieces of 1 KB 46 us, the
+// pieces dealt round robin 39.4 us; the pieces held in registers instead, eight
+// loads ahead, 90 us: a warp has too few load scoreboards to wait for one of
+// many).  The stream runs at the rate of memory (58.7 MB in 8.6 us); what is left is
+// 4.6 us a kernel: its launch, the rows' quantisation, the last sums.
 // Where a warp's part of a row ends it adds its lanes up (one integer warp
 // reduction) and adds the sum to the row's accumulator in shared memory;
 // integer sums are exact in any order, so the result does not depend on the

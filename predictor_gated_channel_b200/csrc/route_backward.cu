@@ -346,9 +346,14 @@ cudaError_t launch_route_backward(const RouteShape &s, const void *logits,
                          s.E,    s.k,     s.sigmoid, s.renorm, s.scale};
   const bool dense = dscores != nullptr || (!s.sigmoid && !s.renorm);
   const bool vectors = aligned16({logits, dscores, dlogits});
-  // Many rows: eight lanes each (32768 x 128 with dscores, bf16 9.6 us against
-  // 16.9, float32 12.3 against 16.1; 2048 x 64 3.1 against 2.7).
-  if (dense && s.T >= 8192 && s.k <= kRowLanes && s.E <= 256) {
+  // Many rows: eight lanes each.  us with dscores, k 8, against a warp a row at 2048 /
+  // 8192 / 32768 rows: bf16 64 experts 3.5 / 4.0 / 6.7 against 3.0 / 5.1 / 13.6, 128 3.6 /
+  // 5.0 / 10.1 against 3.0 / 6.1 / 17.4, 256 5.0 / 8.3 / 23.9 against 4.0 / 9.1 / 28.7;
+  // float32 64 3.4 / 4.6 / 8.6 against 3.1 / 6.2 / 16.9, 192 5.5 / 8.0 / 25.0 against 4.0 /
+  // 9.5 / 28.5; but of 256 (a lane's part a whole 128-byte line, in vectors) 6.1 / 11.7 /
+  // 36.0 against 4.1 / 10.2 / 29.7.
+  const bool lines = vectors && !s.bf16 && s.E == 32 * kRowLanes;  // (not built below)
+  if (dense && s.T >= 8192 && s.k <= kRowLanes && s.E <= 256 && !lines) {
     auto go = [&](auto v) {
       constexpr int V = decltype(v)::value;
       auto launch = [&](auto *kern) {
@@ -358,8 +363,9 @@ cudaError_t launch_route_backward(const RouteShape &s, const void *logits,
       if (s.bf16)
         return blocked ? launch(k_route_bwd_lanes<true, V, true>)
                        : launch(k_route_bwd_lanes<true, V, false>);
-      return blocked ? launch(k_route_bwd_lanes<false, V, true>)
-                     : launch(k_route_bwd_lanes<false, V, false>);
+      if constexpr (V < 32)
+        if (blocked) return launch(k_route_bwd_lanes<false, V, true>);
+      return launch(k_route_bwd_lanes<false, V, false>);
     };
     if (s.E <= 64) return go(std::integral_constant<int, 8>{});
     if (s.E <= 128) return go(std::integral_constant<int, 16>{});

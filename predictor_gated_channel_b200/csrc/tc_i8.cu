@@ -250,8 +250,8 @@ __device__ __forceinline__ uint16_t bf16_bits(float f) {
 }
 
 // Epilogue warps: 16 where a wide SwiGLU tile takes all of TMEM, so that the
-// MMAs wait for half as long (64 experts of 4096 x 1792 with 512 rows each: 789
-// us against 851 with 8), else 8 (8 rows an expert: 235 us against 245 with 16).
+// MMAs wait for half as long (64 experts of 4096 x 1792 with 128 rows each: 346
+// us against 357 with 8), else 8 (8 rows an expert: 235 us against 241 with 16).
 template <bool kSwiGlu, Span kSpan>
 constexpr int epi_warps() {
   return kSwiGlu && kSpan == Span::kPair ? 16 : 8;
@@ -746,12 +746,12 @@ namespace {
 // the tile is as wide as twice the average asks for, so that a decode batch does
 // not pay for a prefill's stages and seldom reads an expert's weights twice.
 // With 64 and more, pairs of 256 rows where they run long and fill the SMs one
-// and a half times: of 64 experts of 4096 x 1792, 128 rows each, 323 us against
-// 332 (SwiGLU) and 347 (down) with one CTA a tile; but single CTAs of 128 rows
+// and a half times: of 64 experts of 4096 x 1792, 128 rows each, 346 us against
+// 356 (SwiGLU) and 347 (down) with one CTA a tile; but single CTAs of 128 rows
 // (SwiGLU) or 256 (down), or of 64 where those would not fill half of the SMs, for
-// short products and few tiles: 64 experts of 576 x 416, 150 rows, 77 against 82
-// us; 8 of 2048 x 1024, 128 rows, 42 against 46; 2 of 1712 x 224, 960 rows, 36
-// against 43.
+// short products and few tiles: 64 experts of 576 x 416, 150 rows, 74 against 83
+// us; 8 of 2048 x 1024, 128 rows, 40 against 44; 2 of 1712 x 224, 960 rows, 35 against
+// 41.
 Tiling grouped_tiling(const ExpertShape &s, int n, int k, int num_w, int num_sms) {
   const int64_t slots = s.slots(), rows = slots / s.E;
   if (rows < 32) return tile_rows(2 * rows + 16, 256, false, true);

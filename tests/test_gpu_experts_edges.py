@@ -441,3 +441,34 @@ def test_route_softmax_rows_of_nothing_but_nan(T, E, dtype):
             assert torch.isnan(got[bad]).all() and torch.isfinite(got[good]).all()
             got = sfn.route_experts_backward(logits.to(DEV), e, dw, renormalize=renorm)
             assert torch.isnan(got[bad]).all() and torch.isfinite(got[good]).all()
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("T,E", [(9000, 160), (9000, 200), (8193, 256), (70, 256)])
+def test_route_backward_of_any_alignment(T, E, score, dtype):
+    """Dense gradients with 16-byte loads and without, around the sizes where the
+    kernels change (tolerances as in test_route_backward_of_tiny_scores)."""
+    k = 6
+    logits = rand(E, T, E, scale=2.0).to(dtype)
+    experts = torch.topk(logits.float(), k, dim=1).indices.to(torch.int32)
+    experts[::5, 2] = -1
+    dw, ds = rand(7, T, k), rand(8, T, E)
+    s, n, v, at = parts_of_gradient(logits, experts, dw, score)
+    big, d = dw.double().abs().amax(1, keepdim=True), ds.double()
+    ref = torch.zeros_like(s).scatter_add(1, at, v * (experts >= 0))
+    tol = torch.zeros_like(s).scatter_add(1, at, 322 * U * n * big)
+    if score == "softmax":
+        ref += s * (d - (s * d).sum(1, keepdim=True))
+    else:
+        ref += s * torch.sigmoid(-logits.double()) * d
+    tol += 200 * U * s * d.abs().amax(1, keepdim=True) + 1e-37
+    if dtype == torch.bfloat16:
+        tol += BF16 * ref.abs()
+    for by in (0, 1):
+        out = offset_view(torch.empty(T, E, dtype=dtype, device=DEV), by)
+        got = sfn.route_experts_backward(offset_view(logits.to(DEV), by), experts.to(DEV),
+                                         dw.to(DEV), dscores=offset_view(ds.to(DEV), by),
+                                         score=score, dlogits=out)
+        assert got.data_ptr() == out.data_ptr()
+        assert ((got.cpu().double() - ref).abs() <= tol).all()
