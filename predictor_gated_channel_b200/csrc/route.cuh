@@ -18,7 +18,7 @@
 // a bound on the error of c; what is inside the bound is decided again in float64.
 //
 // One warp per row, V = E / 32 (rounded up to a built one) values a lane.
-// What bounds it is instruction issue, so the picks run on packed keys: the
+// With whole keys instruction issue bounded it; the picks run on packed keys: the
 // score's order key with the value's place in its lane in the low bits, one
 // 32-bit word.  A lane sorts its V words once (a register network); a pick is
 // then one warp maximum (redux) over the lanes' heads, and the lane that had it
