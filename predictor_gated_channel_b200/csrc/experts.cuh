@@ -46,6 +46,16 @@ cudaError_t launch_i8_gemm(const I8Shape &s, const DeviceInfo &dev, const int8_t
                            const float *sx, const int8_t *wq, const float *sw, void *y,
                            bool weights_early, cudaStream_t st);
 
+// An integer sum times its row's and its channel's scale.  The row's first, but
+// where that passes float32's range (a row that holds a type's lowest value as a
+// mask has a scale of 2^121) the channel's.
+#ifdef __CUDACC__
+__device__ __forceinline__ float scaled_sum(float acc, float row, float channel) {
+  const float t = __fmul_rn(acc, row);
+  return fabsf(t) == INFINITY ? __fmul_rn(__fmul_rn(acc, channel), row) : __fmul_rn(t, channel);
+}
+#endif
+
 // For a few tokens: the quantisation and the product in one kernel that
 // streams the weight rows.
 constexpr int kGemvTokens = 4;
@@ -74,8 +84,8 @@ cudaError_t launch_i8_experts_down(const ExpertShape &s, const DeviceInfo &dev,
 // What follows the integer sums is the same in the tiles and in the streams
 // below, operation by operation, so that a token's bits do not depend on how many
 // tokens share the call:
-//   g = (float)acc sx sg, u likewise; h = bf16(swiglu_f32(g, u))
-//   o = (float)acc sh sd; y = bf16(the sum of fmaf(w, o, .) in slot order)
+//   g = scaled_sum(acc, sx, sg), u likewise; h = bf16(swiglu_f32(g, u))
+//   o = scaled_sum(acc, sh, sd); y = bf16(the sum of fmaf(w, o, .) in slot order)
 // silu(g) u, rounded once, to bf16, by the caller: the element type the FFN's
 // activations have in this library, and what is requantised.  The fast exponential
 // is off by at most (2 + 1.2 |g|) 2^-23, the quotient by 2^-22: together below 2^-16

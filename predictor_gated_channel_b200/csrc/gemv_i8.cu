@@ -342,7 +342,7 @@ __global__ void __launch_bounds__(kThreads)
   __syncthreads();
   for (int i = threadIdx.x; i < rows * T; i += kThreads) {
     const int t = i / rows, v = i - t * rows;
-    const float r = (float)acc[v * kTok + t] * sx[t] * scale[v];
+    const float r = scaled_sum((float)acc[v * kTok + t], sx[t], scale[v]);
     const int64_t o = (int64_t)t * N + n0 + v;
     if (kOutBf16)
       static_cast<uint16_t *>(y)[o] = f32_to_bf16_bits(r);
@@ -398,7 +398,8 @@ __global__ void __launch_bounds__(kThreads)
     const int u = u0 + i, s = u / f;
     const float a = sx[s / k];
     const float2 w = scale[i];
-    const float g = (float)acc[2 * i] * a * w.x, up = (float)acc[2 * i + 1] * a * w.y;
+    const float g = scaled_sum((float)acc[2 * i], a, w.x);
+    const float up = scaled_sum((float)acc[2 * i + 1], a, w.y);
     h[u] = ids[s] < 0 ? (uint16_t)0 : f32_to_bf16_bits(swiglu_f32(g, up));
   }
 }
@@ -454,7 +455,7 @@ __global__ void __launch_bounds__(kThreads)
     for (int j = 0; j < k; ++j)
       if (ids[t * k + j] >= 0)
         s = __fmaf_rn(slot_weight[t * k + j],
-                      (float)acc[i * k + j] * sh[t * k + j] * scale[i * k + j], s);
+                      scaled_sum((float)acc[i * k + j], sh[t * k + j], scale[i * k + j]), s);
     y[u] = f32_to_bf16_bits(s);
   }
 }

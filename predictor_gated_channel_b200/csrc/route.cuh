@@ -513,7 +513,8 @@ __device__ __noinline__ int settle_row(const RouteParams &p, int64_t t, double *
       if (lo > -INFINITY && hi > -INFINITY) {
         // a group's score sums at most two, each at most the largest score
         const float s = p.sigmoid ? 1.f : (z > 0.f ? __fdividef(1.f, z) : 0.f);
-        unsure |= !(lo - hi > 2.f * (score_error(s, lo, p.sigmoid) + score_error(s, hi, p.sigmoid)) +
+        unsure |= !(lo - hi > 2.f * (score_error(s, lo, p.sigmoid) +
+                                     score_error(s, hi, p.sigmoid)) +
                                   4.f * kUlp * (fabsf(lo) + fabsf(hi)));
       }
       if (!__any_sync(kFull, unsure)) return pick;

@@ -357,7 +357,8 @@ cudaError_t launch_route_backward(const RouteShape &s, const void *logits,
     auto go = [&](auto v) {
       constexpr int V = decltype(v)::value;
       auto launch = [&](auto *kern) {
-        return launch_rows(kern, (s.T + 3) / 4, lanes_blocks<V, Lanes::kGradient>(), 0, num_sms, st, p);
+        return launch_rows(kern, (s.T + 3) / 4, lanes_blocks<V, Lanes::kGradient>(), 0, num_sms,
+                           st, p);
       };
       const bool blocked = vectors && s.E == kRowLanes * V;
       if (s.bf16)

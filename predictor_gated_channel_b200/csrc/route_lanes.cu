@@ -255,7 +255,8 @@ cudaError_t launch_route_lanes(const RouteParams &p, bool by_logit, int num_sms,
     auto launch = [&](auto logit, auto grouped) {
       return launch_rows(
           k_route_lanes<kBf16, V, decltype(logit)::value, decltype(grouped)::value>,
-          (p.T + 3) / 4, lanes_blocks<V, route_kind<decltype(logit)::value>()>(), smem, num_sms, st, p);
+          (p.T + 3) / 4, lanes_blocks<V, route_kind<decltype(logit)::value>()>(), smem, num_sms,
+          st, p);
     };
     if (groups) return launch(std::true_type{}, std::true_type{});
     return by_logit ? launch(std::true_type{}, std::false_type{})

@@ -269,6 +269,26 @@ __device__ __forceinline__ auto out_value(float y) {
     return y;
 }
 
+// The epilogue's stores of a lane's channel for 32 rows (n of them; sx: of the
+// lane's row), with scaled_sum(); rare.
+struct Chunk {
+  uint32_t v[32];
+};
+template <bool kSwiGlu, Out kOut, class Elt>
+__device__ __noinline__ void store_scaled(Chunk v, Chunk u, float sx, float sw, float sw2,
+                                          Elt *dst, int stride, int n) {
+#pragma unroll 1
+  for (int i = 0; i < 32; ++i, dst += stride) {
+    const float a = __shfl_sync(kFull, sx, i), x = scaled_sum((float)(int)v.v[i], a, sw);
+    Elt y;
+    if constexpr (kSwiGlu)
+      y = bf16_bits(swiglu_f32(x, scaled_sum((float)(int)u.v[i], a, sw2)));
+    else
+      y = out_value<kOut>(x);
+    if (i < n) *dst = y;
+  }
+}
+
 template <bool kSwiGlu, Out kOut, Span kSpan>
 __global__ void __launch_bounds__((block_threads<kSwiGlu, kSpan>()), 1)
     k_i8_gemm(const __grid_constant__ CUtensorMap tX, const __grid_constant__ CUtensorMap tW,
@@ -498,6 +518,19 @@ __global__ void __launch_bounds__((block_threads<kSwiGlu, kSpan>()), 1)
         }
         using Elt = std::conditional_t<kOut == Out::kF32, float, uint16_t>;
         Elt *dst = static_cast<Elt *>(p.out) + (int64_t)row * p.n + ch;
+        // a row of the chunk whose scale may take an integer sum (at most 2^31) past
+        // the range: not here (with the test in these loops, or beside them a third,
+        // a short product takes 7 % more)
+        if (__any_sync(kFull, fabsf(sx[j]) > 0x1p96f)) {
+          Chunk first, second;
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            first.v[i] = v[i];
+            second.v[i] = kSwiGlu ? u[kSwiGlu ? i : 0] : 0u;
+          }
+          store_scaled<kSwiGlu, kOut>(first, second, sx[j], sw, sw2, dst, p.n, valid ? nr : 0);
+          continue;
+        }
         auto value = [&](int i) -> Elt {
           const float x = (float)(int)v[i];
           if constexpr (kSwiGlu) {
@@ -554,7 +587,7 @@ __global__ void __launch_bounds__((block_threads<kSwiGlu, kSpan>()), 1)
 #pragma unroll
         for (int j = 0; j < 4; ++j)
           if (c + j < chans) {
-            const float y = (float)acc4[j] * sx * __ldg(p.sw + t.ch0 + c + j);
+            const float y = scaled_sum((float)acc4[j], sx, __ldg(p.sw + t.ch0 + c + j));
             using Elt = decltype(out_value<kOut>(y));
             static_cast<Elt *>(p.out)[o + j] = out_value<kOut>(y);
           }

@@ -12,8 +12,8 @@ import torch
 import predictor_gated_channel_b200 as sfn
 from predictor_gated_channel_b200 import _capi
 from predictor_gated_channel_b200 import build as sfn_build
-from test_gpu_experts import (BF16, DEV, U, expert_weights, rand, ref_quantize, ref_route,
-                              ref_scores, weights_i8)
+from test_gpu_experts import (BF16, DEV, U, expert_weights, rand, ref_experts, ref_quantize,
+                              ref_route, ref_scores, weights_i8)
 
 pytestmark = pytest.mark.gpu
 
@@ -472,3 +472,48 @@ def test_route_backward_of_any_alignment(T, E, score, dtype):
                                          score=score, dlogits=out)
         assert got.data_ptr() == out.data_ptr()
         assert ((got.cpu().double() - ref).abs() <= tol).all()
+
+
+# ------------------------------------------------- scales at the end of the range
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("T,N,K", [(1, 300, 4096), (2, 129, 1040), (4, 64, 64), (64, 256, 8192),
+                                   (300, 200, 1040), (2100, 7200, 144)])
+def test_products_of_rows_with_the_lowest_value(T, N, K, dtype):
+    """A row that holds its type's lowest value (a mask) has a scale near 2^121: the
+    integer sum times it passes float32's range, the product with the channel's
+    scale, which is finite, does not.  Channels of zeros give 0 there."""
+    x = rand(T, T, K).to(dtype)
+    x[0, 3] = torch.finfo(dtype).min
+    x[T - 1, K - 1] = torch.finfo(dtype).min / 2
+    wq, sw = weights_i8(5, N, K)
+    wq[1], sw[1] = 0, 0.0
+    sw[2] = 0.0
+    sw = sw * 1e-2
+    q, s = sfn.quantize_rows_i8(x.to(DEV))
+    rq, rs = ref_quantize(x)
+    assert torch.equal(q.cpu().double(), rq)
+    ref = (rq @ wq.double().T) * rs[:, None] * sw.double()
+    assert (ref.abs() < 3e38).all() and ref.abs().max() > 1e33
+    for out in (torch.float32, torch.bfloat16):
+        y = sfn.linear_i8(x.to(DEV), wq.to(DEV), sw.to(DEV), out_dtype=out)
+        tol = 5 * U + (BF16 if out == torch.bfloat16 else 0)
+        assert ((y.cpu().double() - ref).abs() <= tol * ref.abs() + 1e-37).all()
+        z = sfn.matmul_i8(q, s, wq.to(DEV), sw.to(DEV), out_dtype=out)
+        assert torch.equal(z, y)
+
+
+@pytest.mark.parametrize("T", [3, 300])
+def test_experts_of_rows_with_the_lowest_value(T):
+    E, k, d, f = 4, 2, 256, 112
+    W = expert_weights(2, E, f, d)
+    W["sg"] *= 1e-30
+    W["su"] *= 1e-30
+    x = rand(T, T, d).to(torch.bfloat16)
+    x[1, 3] = torch.finfo(torch.bfloat16).min
+    x = x.to(DEV)
+    experts = (torch.arange(k * T, device=DEV) % E).to(torch.int32).view(T, k)
+    weights = torch.rand((T, k), generator=torch.Generator().manual_seed(1)).to(DEV)
+    y = sfn.experts_i8_forward(x, experts, weights, **W)
+    ref, room = ref_experts(x, experts, weights, W)
+    assert ref[1].abs().max() > 1e3 and torch.isfinite(y).all()
+    assert ((y[1].double() - ref[1]).abs() <= (BF16 + 100 * U) * ref[1].abs() + room[1]).all()
